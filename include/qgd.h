@@ -317,6 +317,104 @@ QGD_API qgd_status qlinear_nvfp4_bf16(const void* x_bf16, int ldx, const void* w
                                       void* stream);
 
 /* ---------------------------------------------------------------------
+ * Mixture of experts: the linear layers of a model whose tokens each pass
+ * through a few of E experts (the pages' models are dense; this is the
+ * library's own extension of the same layer).  The calls, in the order a
+ * layer makes them:
+ *   moe_route               which experts a token takes, with which weights
+ *   moe_sort                the (token, expert) pairs in expert order
+ *   qlinear_experts_bf16    gate and up projections of the pairs' tokens,
+ *                           with the gated activation
+ *   qlinear_experts_bf16    down projection of the sorted rows
+ *   moe_combine             the weighted sum of each token's rows
+ * A pair is a (token, slot) with index t * top_k + slot.  None of the calls
+ * reads device data on the host: a run of them can be captured into a CUDA
+ * graph and replayed with other routings.  Workspaces of these calls need no
+ * zero-filling, hold nothing between calls, and must not be shared by calls
+ * that may overlap.  All results are deterministic.
+ * ------------------------------------------------------------------- */
+typedef enum { QGD_DTYPE_BF16 = 0, QGD_DTYPE_FP32 = 1 } qgd_dtype;
+typedef enum { QGD_SCORE_SOFTMAX = 0, QGD_SCORE_SIGMOID = 1 } qgd_score;
+typedef enum { QGD_ACT_NONE = 0, QGD_ACT_SILU_MUL = 1 } qgd_act;
+#define QGD_MAX_EXPERTS 1024
+#define QGD_MAX_TOP_K 32
+#define QGD_MAX_EXPERT_GROUPS 32
+
+typedef struct {
+  int top_k;        /* experts per token, 1..QGD_MAX_TOP_K, at most topk_groups * E / groups */
+  int score;        /* qgd_score */
+  int groups;       /* equal runs of consecutive experts, 1..QGD_MAX_EXPERT_GROUPS, dividing E */
+  int topk_groups;  /* groups that stay in the choice, 1..groups */
+  int group_top;    /* a group's value: its largest choice value (1), or the sum of its two largest (2; of
+                       the only one if just one expert of the group can be chosen) */
+  int renormalize;  /* nonzero: divide the weights by their sum over the chosen experts */
+  float scale;      /* factor of the weights */
+} qgd_route;
+
+/* Expert choice.  logits [T] rows of E values, `ldl` elements apart, in
+ * logits_dtype; bias [E] fp32 or NULL; weights [T][top_k] fp32 and ids
+ * [T][top_k] int32, largest choice value first.
+ *     s = softmax(logits) over the row, or sigmoid(logits)
+ *     choice value = s + bias;  the topk_groups groups of largest value stay;
+ *     ids = the top_k experts of largest choice value in them
+ *     weights = scale * s[ids]  (/ sum of s[ids])
+ * The bias steers the choice only.  Ties go to the lowest index.  Scores and
+ * choice values are compared in 64 bits (without a bias by the logits, whose
+ * order is the scores'; a group_top of 2 adds scores), so the choice does
+ * not depend on how an exponential rounds.  A logit of -inf or NaN (or a bias
+ * that makes the choice value -inf or NaN) keeps its expert from being
+ * chosen; +inf counts as the largest fp32.  Slots left without an expert get
+ * id -1 and weight 0.  1 <= E <= QGD_MAX_EXPERTS; ldl >= E; logits aligned to
+ * their type. */
+QGD_API qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl, const float* bias,
+                             const qgd_route* route, float* weights, int* ids, void* stream);
+
+/* Stable sort of the pairs by expert.  ids [pairs] int32; an id outside
+ * [0, E) drops its pair.  offsets [E + 1]: expert e's pairs are the sorted
+ * positions offsets[e] .. offsets[e+1] - 1; order [pairs]: the pair at each
+ * sorted position, -1 behind the last; pos [pairs]: the sorted position of
+ * each pair, -1 where it was dropped.  pairs == 0 writes offsets only (all
+ * zero).  Workspace: qgd_moe_sort_workspace_size() bytes, 4-byte aligned
+ * (NULL when 0). */
+QGD_API size_t qgd_moe_sort_workspace_size(int pairs, int E);
+QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Grouped layer call: the rows of each expert times that expert's weights.
+ * For the sorted rows i = offsets[e] .. offsets[e+1] - 1 of expert e, with
+ * source row r = order[i] / top_k (order NULL: r = i, top_k ignored):
+ *     v = dequant(quantize(x[r])) . dequant(wq[e])^T
+ *     QGD_ACT_NONE:      y[i] = bf16(v)                      wq [E][N][K]
+ *     QGD_ACT_SILU_MUL:  y[i] = bf16(silu(v[0..N)) * v[N..2N))
+ *                        silu(g) = g / (1 + exp(-g))         wq [E][2N][K]
+ * with the codes and scales of quant_act_per_token and fp32 (int32)
+ * accumulation, the activation taken of the fp32 values.
+ *   fmt      QGD_FMT_FP8_DYNAMIC or QGD_FMT_W8A8_INT8 (others ->
+ *            QGD_ERR_UNSUPPORTED)
+ *   x        bf16, x_rows rows ldx elements apart (ldx >= K, ldx % 8 == 0)
+ *   rows     length of order and of y; rows of y at offsets[E] and behind are
+ *            left as they were
+ *   sw       fp32 [E][N] (or [E][2N])
+ * Offsets are read on the device, clamped to [0, rows]; a source row outside
+ * [0, x_rows) counts as zeros.  N % 16 == 0; K % 16 == 0, K <= 16384;
+ * 1 <= E <= QGD_MAX_EXPERTS.  x, wq, y and ws 16-byte aligned.  y must not
+ * overlap the inputs. */
+QGD_API size_t qgd_experts_workspace_size(int fmt, int rows, int E, int N, int K, int act);
+QGD_API qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows, const int* order, int top_k,
+                                        const int* offsets, int E, int rows, const void* wq, const float* sw,
+                                        void* y_bf16, int N, int K, int act, void* ws, size_t ws_bytes, void* stream);
+
+/* Weighted sum of each token's expert outputs, in slot order in fp32:
+ *     y[t] = bf16( add[t] + sum_j weights[t][j] * h[pos[t][j]] )
+ * over the slots with 0 <= pos < rows (a dropped pair's weight is not read).
+ * h bf16 [rows][H]; pos int32 and weights fp32 [T][top_k]; add bf16 [T]
+ * rows lda elements apart, or NULL for zero; y bf16 [T][H].  H % 8 == 0;
+ * top_k <= QGD_MAX_TOP_K; h, add and y 16-byte aligned, lda % 8 == 0.  y may
+ * be add, and must not overlap h. */
+QGD_API qgd_status moe_combine(const void* h_bf16, int rows, const int* pos, const float* weights,
+                               const void* add_bf16, int lda, void* y_bf16, int T, int top_k, int H, void* stream);
+
+/* ---------------------------------------------------------------------
  * Column-parallel (tensor-parallel) layer call with the all-gather fused
  * into the GEMM's output stores.  The pages run one GPU only (tensor
  * parallelism of one: "Building a High-Performance and Portable vLLM Linear

@@ -8,7 +8,8 @@ streams.  The functions keep the C names:
     qlinear_fp8_dynamic, qlinear_w8a8_int8, qlinear_block_fp8,
     qgd_w8a8_int8_acc32, qgd_workspace_size, qgd_load_dispatch_table,
     qgd_clear_dispatch_table, qgd_set_override, qgd_get_plan, qgd_m_bucket,
-    qgd_device_error, qgd_clear_device_error
+    qgd_device_error, qgd_clear_device_error,
+    moe_route, moe_sort, qlinear_experts_bf16, moe_combine
 
 There is no fallback: if libqgd.so is missing or cannot be loaded, every call
 raises.
@@ -39,6 +40,9 @@ __all__ = [
     "MAX_TP_RANKS", "qlinear_tp_bf16", "qgd_tp_workspace_size", "qgd_tp_wait", "ipc_malloc", "ipc_open",
     "ipc_close", "ipc_free", "tensor_at",
     "Workspace", "DEFAULT_TABLE",
+    "ACT_NONE", "ACT_SILU_MUL", "MAX_EXPERTS", "MAX_TOP_K", "MAX_EXPERT_GROUPS",
+    "moe_route", "moe_sort", "qlinear_experts_bf16", "moe_combine",
+    "qgd_moe_sort_workspace_size", "qgd_experts_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +56,8 @@ QTYPE_E4M3, QTYPE_INT8 = 0, 1
 VARIANT_STANDARD, VARIANT_SWAP_AB, VARIANT_STANDARD_PAIR = 0, 1, 2
 REDUCE_LAST_CTA, REDUCE_TWO_PASS, REDUCE_ATOMIC, REDUCE_CLUSTER = 0, 1, 2, 3
 SCHEDULE_GRID, SCHEDULE_PERSISTENT = 0, 1
+ACT_NONE, ACT_SILU_MUL = 0, 1
+MAX_EXPERTS, MAX_TOP_K, MAX_EXPERT_GROUPS = 1024, 32, 32
 FORMAT_NAMES = {"fp8_dynamic": 0, "w8a8_int8": 1, "block_fp8": 2, "mxfp8": 3}
 
 _lock = threading.Lock()
@@ -71,6 +77,12 @@ IPC_HANDLE_BYTES = 64
 class _Tp(ctypes.Structure):
     _fields_ = [("ranks", ctypes.c_int), ("rank", ctypes.c_int), ("col0", ctypes.c_int), ("ldy", ctypes.c_int),
                 ("y", ctypes.c_void_p * MAX_TP_RANKS), ("flags", ctypes.c_void_p * MAX_TP_RANKS)]
+
+
+class _Route(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int),
+                ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 class _Plan(ctypes.Structure):
@@ -129,6 +141,10 @@ def lib() -> ctypes.CDLL:
             "qgd_ipc_open": [P, ctypes.POINTER(ctypes.c_void_p)],
             "qgd_ipc_close": [P],
             "qgd_ipc_free": [P],
+            "moe_route": [P, I, I, I, I, P, ctypes.POINTER(_Route), P, P, P],
+            "moe_sort": [P, I, I, P, P, P, P, S, P],
+            "qlinear_experts_bf16": [I, P, I, I, P, I, P, I, I, P, P, P, I, I, I, P, S, P],
+            "moe_combine": [P, I, P, P, P, I, P, I, I, I, P],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -140,6 +156,10 @@ def lib() -> ctypes.CDLL:
         L.qgd_layer_workspace_size.restype = S
         L.qgd_tp_workspace_size.argtypes = [I, I, I, I]
         L.qgd_tp_workspace_size.restype = S
+        L.qgd_moe_sort_workspace_size.argtypes = [I, I]
+        L.qgd_moe_sort_workspace_size.restype = S
+        L.qgd_experts_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.qgd_experts_workspace_size.restype = S
         L.qgd_m_bucket.argtypes = [I]
         L.qgd_m_bucket.restype = I
         L.qgd_status_string.argtypes = [I]
@@ -669,6 +689,220 @@ def qgd_w8a8_int8_acc32(xq, wq, acc=None, ws=None, stream=None):
     _check(lib().qgd_w8a8_int8_acc32(_ptr(xq), _ptr(wq), _ptr(acc), M, N, K, ctypes.c_void_p(wsp), wsn,
                                      _stream(stream)), "qgd_w8a8_int8_acc32")
     return acc
+
+
+# ---------------------------------------------------------------------------
+# Mixture of experts
+# ---------------------------------------------------------------------------
+class _On:
+    """The device and stream of one call: the tensors' device made current if
+    it is not, allocations on the call's stream, so that a workspace or an
+    output made here belongs to the stream that uses it (and to the capture's
+    memory pool while a graph is captured)."""
+
+    def __init__(self, device, stream):
+        self.device = device.index if device.index is not None else torch.cuda.current_device()
+        self.guards = []
+        if self.device != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(self.device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _operand(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a tensor of type {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor with unit column stride (dense, or a column
+    slice of a wider matrix)."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} must have a row stride of at least its {cols} columns")
+    return t.stride(0)
+
+
+def _scratch(ws, need: int, device):
+    """(pointer, bytes) of a workspace that needs no zero-filling: the
+    caller's, or one of this call's own."""
+    if need == 0:
+        return None, 0, None
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif isinstance(ws, Workspace):
+        ws = ws.ensure(need).buf
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=None, groups: int = 1,
+              topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+              weights=None, ids=None, stream=None):
+    """Expert choice: logits [T, E] (bf16 or fp32; may be a column slice of a
+    wider matrix) -> (weights fp32 [T, top_k], ids int32 [T, top_k]), largest
+    choice value first, ties to the lowest expert.
+
+    Scores are softmax(logits) over the row or sigmoid(logits); the choice is
+    by score + bias (fp32 [E]; it steers the choice only) among the experts of
+    the topk_groups best of `groups` equal groups, a group's value being its
+    largest choice value (group_top 1) or the sum of its two largest (2).  The
+    weights are the chosen scores, divided by their sum if renormalize, times
+    scale.  A logit of -inf or NaN keeps its expert out; slots left without an
+    expert get id -1 and weight 0."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}")
+    _operand(logits, "logits", (torch.bfloat16, torch.float32), contiguous=False)
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    T, E = logits.shape
+    dev = logits.device
+    ldl = _row_stride(logits, "logits")
+    if bias is not None:
+        _operand(bias, "bias", (torch.float32,), (E,), dev)
+    r = _Route(top_k, _SCORES[score], groups, topk_groups, group_top, 1 if renormalize else 0, scale)
+    with _On(dev, stream) as s:
+        if weights is None:
+            weights = torch.empty((T, top_k if top_k > 0 else 0), dtype=torch.float32, device=dev)
+        if ids is None:
+            ids = torch.empty((T, top_k if top_k > 0 else 0), dtype=torch.int32, device=dev)
+        _operand(weights, "weights", (torch.float32,), (T, max(top_k, 0)), dev)
+        _operand(ids, "ids", (torch.int32,), (T, max(top_k, 0)), dev)
+        _check(lib().moe_route(_ptr(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, ldl, _ptr(bias),
+                               ctypes.byref(r), _ptr(weights), _ptr(ids), s), "moe_route")
+    return weights, ids
+
+
+def qgd_moe_sort_workspace_size(pairs: int, E: int) -> int:
+    return int(lib().qgd_moe_sort_workspace_size(pairs, E))
+
+
+def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=None, ws=None, stream=None):
+    """Stable sort of the (token, slot) pairs by expert: ids int32 [T, top_k]
+    (or any shape) -> (offsets int32 [E + 1], order int32 [pairs], pos int32
+    like ids).  Expert e's pairs sit at sorted positions offsets[e] ..
+    offsets[e + 1] - 1; order is the pair at each position (-1 behind the
+    last), pos the position of each pair.  An id outside [0, E) drops its pair
+    (pos -1)."""
+    _operand(ids, "ids", (torch.int32,))
+    dev, P = ids.device, ids.numel()
+    with _On(dev, stream) as s:
+        if offsets is None:
+            offsets = torch.empty((max(num_experts, 0) + 1,), dtype=torch.int32, device=dev)
+        if order is None:
+            order = torch.empty((P,), dtype=torch.int32, device=dev)
+        if pos is None:
+            pos = torch.empty_like(ids)
+        _operand(offsets, "offsets", (torch.int32,), (max(num_experts, 0) + 1,), dev)
+        _operand(order, "order", (torch.int32,), (P,), dev)
+        _operand(pos, "pos", (torch.int32,), tuple(ids.shape), dev)
+        wsp, wsn, _keep = _scratch(ws, qgd_moe_sort_workspace_size(P, num_experts), dev)
+        _check(lib().moe_sort(_ptr(ids), P, num_experts, _ptr(offsets), _ptr(order), _ptr(pos), wsp, wsn, s),
+               "moe_sort")
+    return offsets, order, pos
+
+
+def qgd_experts_workspace_size(fmt: int, rows: int, E: int, N: int, K: int, act: int = ACT_NONE) -> int:
+    return int(lib().qgd_experts_workspace_size(fmt, rows, E, N, K, act))
+
+
+def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None, top_k: int = 1,
+                         act: int = ACT_NONE, y=None, ws=None, stream=None):
+    """Grouped layer call: y bf16 [rows, N], each expert's rows times its own
+    weights, with dynamic quantization of x.
+
+    wq [E, N, K] int8 or e4m3 and sw fp32 [E, N] (W8A8_INT8, FP8_Dynamic;
+    per-channel quantization of each expert's weights); with ACT_SILU_MUL
+    wq holds [E, 2N, K], gate rows before up rows, and y = silu(gate) * up.
+    offsets and order as moe_sort gives them: sorted row i takes x row
+    order[i] // top_k, or row i where order is None.  x [*, K] bf16 may be a
+    column slice of a wider matrix.  Rows of y behind the last expert's are
+    left as they were."""
+    if act not in (ACT_NONE, ACT_SILU_MUL):
+        raise ValueError("act must be ACT_NONE or ACT_SILU_MUL")
+    _operand(x, "x", (torch.bfloat16,), contiguous=False)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    x_rows, K = x.shape
+    ldx = _row_stride(x, "x")
+    dev = x.device
+    _operand(wq, "wq", (torch.int8,) if fmt == FMT_W8A8_INT8 else (torch.uint8, torch.float8_e4m3fn), device=dev)
+    if wq.dim() != 3 or wq.shape[2] != K:
+        raise ValueError(f"wq must be [experts, rows, K={K}], got {tuple(wq.shape)}")
+    E, n_all = wq.shape[0], wq.shape[1]
+    if act == ACT_SILU_MUL and n_all % 2:
+        raise ValueError("wq must hold as many up rows as gate rows")
+    N = n_all // 2 if act == ACT_SILU_MUL else n_all
+    _operand(sw, "sw", (torch.float32,), (E, n_all), dev)
+    _operand(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    rows = x_rows
+    if order is not None:
+        _operand(order, "order", (torch.int32,), device=dev)
+        rows = order.numel()
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+        _operand(y, "y", (torch.bfloat16,), (rows, N), dev)
+        wsp, wsn, _keep = _scratch(ws, qgd_experts_workspace_size(fmt, rows, E, N, K, act), dev)
+        _check(lib().qlinear_experts_bf16(fmt, _ptr(x), ldx, x_rows, _ptr(order), top_k, _ptr(offsets), E, rows,
+                                          _ptr(wq), _ptr(sw), _ptr(y), N, K, act, wsp, wsn, s),
+               "qlinear_experts_bf16")
+    return y
+
+
+def moe_combine(h: torch.Tensor, pos, weights, add=None, y=None, stream=None):
+    """Weighted sum of each token's expert outputs: y[t] = add[t] + sum over
+    the slots j with pos[t, j] >= 0 of weights[t, j] * h[pos[t, j]], in fp32,
+    rounded once to bf16.  h bf16 [rows, H]; pos int32 and weights fp32
+    [T, top_k]; add bf16 [T, H] (may be a column slice; may be y itself)."""
+    _operand(h, "h", (torch.bfloat16,))
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D")
+    rows, H = h.shape
+    dev = h.device
+    _operand(pos, "pos", (torch.int32,), device=dev)
+    if pos.dim() != 2:
+        raise ValueError("pos must be [tokens, top_k]")
+    T, k = pos.shape
+    _operand(weights, "weights", (torch.float32,), (T, k), dev)
+    lda = 0
+    if add is not None:
+        _operand(add, "add", (torch.bfloat16,), (T, H), dev, contiguous=False)
+        lda = _row_stride(add, "add")
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _operand(y, "y", (torch.bfloat16,), (T, H), dev)
+        _check(lib().moe_combine(_ptr(h), rows, _ptr(pos), _ptr(weights), _ptr(add), lda, _ptr(y), T, k, H, s),
+               "moe_combine")
+    return y
 
 
 # ---------------------------------------------------------------------------

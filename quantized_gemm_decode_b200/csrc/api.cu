@@ -730,6 +730,50 @@ qgd_status run_layer(int fmt, const void* x_bf16, int ldx, const void* wq, const
 }
 
 // ---------------------------------------------------------------------------
+// Grouped GEMM over experts: plan and workspace (arrival counters, codes,
+// scales, partials of tiles shared by several CTAs).
+// ---------------------------------------------------------------------------
+constexpr int kMaxExpertCtas = 256;  // SMs of any sm_100 part
+
+struct ExpertPlan {
+  int tok = 0, n_tiles = 0, ctas = 0;
+  size_t q_off = 0, s_off = 0, part_off = 0, total = 0;
+};
+
+ExpertPlan expert_plan(int rows, int E, int N, int K, bool act) {
+  ExpertPlan p;
+  // few rows per expert: 64-token tiles whose K range is shared out over all
+  // SMs (weights streamed once bound them); many: 256-token tiles
+  p.tok = rows / (rows < E ? rows : E) < 64 ? 64 : 256;
+  p.n_tiles = act ? (N + 63) / 64 : (N + 127) / 128;
+  p.ctas = g_num_sms < kMaxExpertCtas ? g_num_sms : kMaxExpertCtas;
+  p.q_off = align256(static_cast<size_t>(p.ctas) * 4);
+  p.s_off = align256(p.q_off + static_cast<size_t>(rows) * K);
+  p.part_off = align256(p.s_off + static_cast<size_t>(rows) * 4);
+  p.total = p.part_off + (p.tok <= 64 ? static_cast<size_t>(p.ctas) * 2 * p.tok * kSwapTileN * 4 : 0);
+  return p;
+}
+
+// Expert weights [E][rows][K] as boxes of 128 bytes x 128 rows, or with the
+// gated activation [E][2][N][K] as 128 bytes x 16 gate rows and their 16 up
+// rows; 128-byte swizzle, zeros past the extents.
+qgd_status encode_experts(CUtensorMap* map, const void* base, int E, int N, int K, bool act) {
+  const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), e = static_cast<cuuint64_t>(E);
+  cuuint64_t dims[4] = {k, n, act ? 2 : e, e};
+  cuuint64_t strides[3] = {k, k * n, 2 * k * n};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(kTileK), act ? 16u : 128u, act ? 2u : 1u, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, act ? 4 : 3, const_cast<void*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(QGD_ERR_CUDA, "cuTensorMapEncodeTiled (experts) failed (%d) E=%d N=%d K=%d", (int)r, E, N, K);
+  return QGD_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// ---------------------------------------------------------------------------
 // Built-in scratch for qlinear_fp8_dynamic_noalloc.  Some callers must not
 // allocate device memory once they are running: an engine that carves all
 // device memory into fixed pools at start-up has none left to give, and a
@@ -1004,6 +1048,153 @@ qgd_status qgd_ipc_free(void* dptr) {
   return QGD_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Mixture of experts
+// ---------------------------------------------------------------------------
+static_assert(QGD_MAX_EXPERTS == kMaxExperts && QGD_MAX_TOP_K == kMaxTopK && QGD_MAX_EXPERT_GROUPS == kMaxGroups,
+              "expert limits");
+
+qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl, const float* bias,
+                     const qgd_route* route, float* weights, int* ids, void* stream) {
+  if (!route) return fail(QGD_ERR_INVALID, "null route descriptor");
+  const qgd_route& r = *route;
+  if (T < 0 || E <= 0) return fail(QGD_ERR_INVALID, "bad sizes (T=%d E=%d)", T, E);
+  if (E > kMaxExperts) return fail(QGD_ERR_UNSUPPORTED, "E=%d experts (at most %d)", E, kMaxExperts);
+  if (logits_dtype != QGD_DTYPE_BF16 && logits_dtype != QGD_DTYPE_FP32)
+    return fail(QGD_ERR_INVALID, "bad logits type %d", logits_dtype);
+  if (r.score != QGD_SCORE_SOFTMAX && r.score != QGD_SCORE_SIGMOID) return fail(QGD_ERR_INVALID, "bad score %d", r.score);
+  if (r.groups < 1 || r.groups > kMaxGroups || E % r.groups != 0)
+    return fail(QGD_ERR_INVALID, "%d groups of %d experts (1..%d groups of equal size)", r.groups, E, kMaxGroups);
+  if (r.topk_groups < 1 || r.topk_groups > r.groups)
+    return fail(QGD_ERR_INVALID, "topk_groups=%d of %d groups", r.topk_groups, r.groups);
+  if (r.group_top != 1 && r.group_top != 2) return fail(QGD_ERR_INVALID, "group_top=%d must be 1 or 2", r.group_top);
+  if (r.top_k < 1 || r.top_k > kMaxTopK || r.top_k > r.topk_groups * (E / r.groups))
+    return fail(QGD_ERR_INVALID, "top_k=%d (1..%d, at most the %d experts of %d groups)", r.top_k, kMaxTopK,
+                r.topk_groups * (E / r.groups), r.topk_groups);
+  if (ldl < E) return fail(QGD_ERR_INVALID, "row stride ldl=%d must be >= E=%d", ldl, E);
+  if (T == 0) return QGD_OK;
+  if (!logits || !weights || !ids) return fail(QGD_ERR_INVALID, "null pointer");
+  if (!aligned4(weights) || !aligned4(ids) || !aligned4(bias) ||
+      (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == QGD_DTYPE_FP32 ? 3u : 1u)))
+    return fail(QGD_ERR_INVALID, "logits, bias, weights and ids must be aligned to their types");
+  qgd_status st = check_device();
+  if (st != QGD_OK) return st;
+  RouteArgs a{logits, bias, weights, ids, T, E, ldl, r.top_k, r.score == QGD_SCORE_SIGMOID, r.groups, r.topk_groups,
+              r.group_top, r.renormalize != 0, r.scale};
+  const cudaError_t e = launch_route(a, logits_dtype == QGD_DTYPE_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_route launch");
+}
+
+size_t qgd_moe_sort_workspace_size(int pairs, int E) {
+  if (pairs <= 0 || E <= 0 || E > kMaxExperts) return 0;
+  const int blocks = sort_blocks(pairs, E);
+  return blocks > 1 ? align256(static_cast<size_t>(blocks) * E * 4) : 0;
+}
+
+qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws, size_t ws_bytes,
+                    void* stream) {
+  if (pairs < 0 || E <= 0) return fail(QGD_ERR_INVALID, "bad sizes (pairs=%d E=%d)", pairs, E);
+  if (E > kMaxExperts) return fail(QGD_ERR_UNSUPPORTED, "E=%d experts (at most %d)", E, kMaxExperts);
+  if (!offsets || (pairs > 0 && (!ids || !order || !pos))) return fail(QGD_ERR_INVALID, "null pointer");
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(pos) || !aligned4(ws))
+    return fail(QGD_ERR_INVALID, "pointers must be 4-byte aligned");
+  const size_t need = qgd_moe_sort_workspace_size(pairs, E);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(QGD_ERR_WORKSPACE, "sort workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : 0);
+  qgd_status st = check_device();
+  if (st != QGD_OK) return st;
+  const cudaError_t e = launch_sort(ids, pairs, E, offsets, order, pos, static_cast<int*>(ws),
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_sort launch");
+}
+
+size_t qgd_experts_workspace_size(int fmt, int rows, int E, int N, int K, int act) {
+  if ((fmt != kFmtFP8 && fmt != kFmtINT8) || rows <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
+  int devices = 0;  // on a GPU host the plan follows the device's SM count, as in the call
+  if (cudaGetDeviceCount(&devices) == cudaSuccess && devices > 0) (void)check_device();
+  else (void)cudaGetLastError();
+  return expert_plan(rows, E, N, K, act == QGD_ACT_SILU_MUL).total;
+}
+
+qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows, const int* order, int top_k,
+                                const int* offsets, int E, int rows, const void* wq, const float* sw, void* y_bf16,
+                                int N, int K, int act, void* ws, size_t ws_bytes, void* stream) {
+  if (fmt < 0 || fmt >= kNumFmts) return fail(QGD_ERR_INVALID, "bad format %d", fmt);
+  if (fmt != kFmtFP8 && fmt != kFmtINT8)
+    return fail(QGD_ERR_UNSUPPORTED, "grouped products cover FP8_Dynamic and W8A8_INT8 (format %d)", fmt);
+  if (act != QGD_ACT_NONE && act != QGD_ACT_SILU_MUL) return fail(QGD_ERR_INVALID, "bad activation %d", act);
+  if (rows < 0 || x_rows < 0 || E <= 0 || N <= 0 || K <= 0)
+    return fail(QGD_ERR_INVALID, "bad sizes (rows=%d x_rows=%d E=%d N=%d K=%d)", rows, x_rows, E, N, K);
+  if (E > kMaxExperts) return fail(QGD_ERR_UNSUPPORTED, "E=%d experts (at most %d)", E, kMaxExperts);
+  if (N % 16 != 0 || K % 16 != 0) return fail(QGD_ERR_UNSUPPORTED, "N=%d and K=%d must be multiples of 16", N, K);
+  if (K > kExpertMaxK) return fail(QGD_ERR_UNSUPPORTED, "K=%d must be <= %d", K, kExpertMaxK);
+  if (ldx < K || ldx % 8 != 0)
+    return fail(QGD_ERR_INVALID, "row stride ldx=%d must be >= K=%d and a multiple of 8", ldx, K);
+  if (order && top_k < 1) return fail(QGD_ERR_INVALID, "top_k=%d must be positive", top_k);
+  if (!order && rows > x_rows) return fail(QGD_ERR_INVALID, "%d rows of %d without an order", rows, x_rows);
+  const long long n_all = static_cast<long long>(N) * (act == QGD_ACT_SILU_MUL ? 2 : 1);
+  if (n_all * E >= (1LL << 30) || (static_cast<long long>(rows) / 64 + E) * ((N + 63) / 64) > (1LL << 31) - 1)
+    return fail(QGD_ERR_UNSUPPORTED, "too many weight rows or tiles (rows=%d E=%d N=%d)", rows, E, N);
+  if (rows == 0) return QGD_OK;
+  if (!x_bf16 || !offsets || !wq || !sw || !y_bf16) return fail(QGD_ERR_INVALID, "null operand pointer");
+  if (!aligned16(x_bf16) || !aligned16(wq) || !aligned16(y_bf16) || !aligned4(order) || !aligned4(offsets) ||
+      !aligned4(sw))
+    return fail(QGD_ERR_INVALID, "x, wq and y must be 16-byte aligned, order, offsets and sw 4-byte aligned");
+  qgd_status st;
+  if ((st = check_device()) != QGD_OK) return st;
+  if ((st = get_encoder()) != QGD_OK) return st;
+  const bool gated = act == QGD_ACT_SILU_MUL;
+  const ExpertPlan p = expert_plan(rows, E, N, K, gated);
+  if (!ws || ws_bytes < p.total)
+    return fail(QGD_ERR_WORKSPACE, "experts workspace of %zu bytes needed, %zu given", p.total, ws ? ws_bytes : 0);
+  if (!aligned16(ws)) return fail(QGD_ERR_INVALID, "workspace must be 16-byte aligned");
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  uint8_t* q = wsb + p.q_off;
+  float* s = reinterpret_cast<float*>(wsb + p.s_off);
+  ExpertArgs a{};
+  a.offsets = offsets;
+  a.sx = s;
+  a.sw = sw;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.partial = reinterpret_cast<uint32_t*>(wsb + p.part_off);
+  a.tickets = reinterpret_cast<unsigned*>(wsb);
+  a.E = E;
+  a.P = rows;
+  a.N = N;
+  a.K = K;
+  a.n_tiles = p.n_tiles;
+  a.tok = p.tok;
+  a.ctas = p.ctas;
+  CUtensorMap tw, tx;
+  if ((st = encode_experts(&tw, wq, E, N, K, gated)) != QGD_OK) return st;
+  if ((st = encode_kmajor(&tx, q, rows, K, p.tok <= 64 ? 16 : 64)) != QGD_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_experts_quant(fmt, a, static_cast<const uint16_t*>(x_bf16), ldx, x_rows, order,
+                                       order ? top_k : 1, q, s, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "experts quantizer launch");
+  e = launch_experts(fmt, gated, tw, tx, a, cs);
+  return e == cudaSuccess ? QGD_OK : cuda_fail(e, "grouped GEMM launch");
+}
+
+qgd_status moe_combine(const void* h_bf16, int rows, const int* pos, const float* weights, const void* add_bf16,
+                       int lda, void* y_bf16, int T, int top_k, int H, void* stream) {
+  if (rows < 0 || T < 0 || H <= 0) return fail(QGD_ERR_INVALID, "bad sizes (rows=%d T=%d H=%d)", rows, T, H);
+  if (top_k < 1 || top_k > kMaxTopK) return fail(QGD_ERR_INVALID, "top_k=%d (1..%d)", top_k, kMaxTopK);
+  if (H % 8 != 0) return fail(QGD_ERR_UNSUPPORTED, "H=%d must be a multiple of 8", H);
+  if (add_bf16 && (lda < H || lda % 8 != 0))
+    return fail(QGD_ERR_INVALID, "row stride lda=%d must be >= H=%d and a multiple of 8", lda, H);
+  if (T == 0) return QGD_OK;
+  if ((!h_bf16 && rows > 0) || !pos || !weights || !y_bf16) return fail(QGD_ERR_INVALID, "null pointer");
+  if (!aligned16(h_bf16) || !aligned16(add_bf16) || !aligned16(y_bf16) || !aligned4(pos) || !aligned4(weights))
+    return fail(QGD_ERR_INVALID, "h, add and y must be 16-byte aligned, pos and weights 4-byte aligned");
+  qgd_status st = check_device();
+  if (st != QGD_OK) return st;
+  const cudaError_t e = launch_combine(static_cast<const uint16_t*>(h_bf16), rows, pos, weights,
+                                       static_cast<const uint16_t*>(add_bf16), lda, static_cast<uint16_t*>(y_bf16), T,
+                                       top_k, H, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_combine launch");
+}
+
 size_t qgd_layer_workspace_size(int fmt, int M, int N, int K) {
   if (fmt < 0 || fmt >= kNumFmts || M <= 0 || N <= 0 || K <= 0) return 0;
   return layer_ws(fmt, M, N, K).total;
@@ -1184,12 +1375,14 @@ qgd_status qgd_device_error(unsigned int* code) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   e = read_device_error(code);
   if (e == cudaSuccess && *code == 0) e = read_probe_error(code);
+  if (e == cudaSuccess && *code == 0) e = read_experts_error(code);
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "read device error flag");
 }
 
 qgd_status qgd_clear_device_error(void) {
   cudaError_t e = clear_device_error();
   if (e == cudaSuccess) e = clear_probe_error();
+  if (e == cudaSuccess) e = clear_experts_error();
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "clear device error flag");
 }
 

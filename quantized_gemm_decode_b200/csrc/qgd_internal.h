@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace qgd {
 
 enum Fmt : int { kFmtFP8 = 0, kFmtINT8 = 1, kFmtBlock = 2, kFmtMX = 3, kFmtNV = 4 };
@@ -117,6 +119,68 @@ int swapab_max_stages(int mpad, int kps, bool cluster, bool fused);
 int standard_max_stages(int tile_n, int kps);
 size_t pair_smem_bytes(int stages, int kps);
 int pair_max_stages(int kps);
+
+// ---------------------------------------------------------------------------
+// Mixture of experts (moe.cu, experts.cu)
+// ---------------------------------------------------------------------------
+// Opt a kernel in to `bytes` of dynamic shared memory, once per device (`done`: a bit per device).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+constexpr int kMaxExperts = 1024;
+constexpr int kExpertMaxK = 16384;  // the sorted rows' quantizer keeps a row in registers
+constexpr int kMaxTopK = 32;
+constexpr int kMaxGroups = 32;
+
+struct RouteArgs {
+  const void* logits;  // [T] rows, ldl elements apart, bf16 or fp32
+  const float* bias;   // [E] or null
+  float* weights;      // [T][k]
+  int* ids;            // [T][k]
+  int T, E, ldl, k;
+  int sigmoid;         // scores: 0 softmax over the row, 1 sigmoid
+  int groups, keep;    // expert groups, and how many of them stay in the choice
+  int top;             // a group's value: its largest choice value (1) or the sum of its two largest (2)
+  int renorm;
+  float scale;
+};
+cudaError_t launch_route(const RouteArgs& a, bool bf16, cudaStream_t stream);
+
+// counts: [blocks][E] scratch of sort_blocks(P, E) blocks (none for one block)
+int sort_blocks(int P, int E);
+cudaError_t launch_sort(const int* ids, int P, int E, int* offsets, int* order, int* pos, int* counts,
+                        cudaStream_t stream);
+cudaError_t launch_combine(const uint16_t* h, int P, const int* pos, const float* weights, const uint16_t* add, int lda,
+                           uint16_t* y, int T, int k, int H, cudaStream_t stream);
+
+// Grouped GEMM over rows sorted by expert.
+struct ExpertArgs {
+  const int* offsets;    // [E + 1] first sorted row of each expert
+  const float* sx;       // [P] scales of the sorted rows' codes
+  const float* sw;       // [E][weight rows]
+  uint16_t* y;           // [P][N]
+  uint32_t* partial;     // split walk: [ctas][2][tok][128] accumulators
+  unsigned int* tickets; // split walk: arrivals at the tile that starts in each CTA (zeroed by the quantizer)
+  int E, P, N, K;        // N: output columns (half the weight rows with the gated activation)
+  int n_tiles;           // weight tiles per expert
+  int tok;               // most token rows per tile
+  int ctas;
+};
+cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
+                                 const int* order, int div, uint8_t* q, float* s, cudaStream_t stream);
+cudaError_t launch_experts(int fmt, bool act, const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a,
+                           cudaStream_t stream);
+cudaError_t read_experts_error(unsigned int* code);
+cudaError_t clear_experts_error();
 
 // Tensor-core peak probe (probe.cu).
 cudaError_t launch_mma_probe(int qtype, int iters, int ctas, cudaStream_t stream);
