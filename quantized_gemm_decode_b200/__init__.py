@@ -16,7 +16,9 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -694,73 +696,85 @@ def qgd_w8a8_int8_acc32(xq, wq, acc=None, ws=None, stream=None):
 # ---------------------------------------------------------------------------
 # Mixture of experts
 # ---------------------------------------------------------------------------
-class _On:
-    """The device and stream of one call: the tensors' device made current if
-    it is not, allocations on the call's stream, so that a workspace or an
-    output made here belongs to the stream that uses it (and to the capture's
-    memory pool while a graph is captured)."""
-
-    def __init__(self, device, stream):
-        self.device = device.index if device.index is not None else torch.cuda.current_device()
-        self.guards = []
-        if self.device != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(self.device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _operand(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be a tensor of type {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_cuda:
+def _on(device: int, stream) -> contextlib.ExitStack:
+    """Device `device` current, and `stream` (or its current stream): the call
+    inside launches there and allocates there, so that a workspace or an output
+    made by it belongs to the stream that uses it (and to the capture's memory
+    pool while a graph is captured)."""
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device.index != device:
+            stack.close()
+            raise ValueError(f"stream is on {stream.device}, the operands on cuda:{device}")
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    return t.get_device()
+
+
+def _operand(t, name: str, dtypes, shape, device: int, contiguous: bool = True) -> int:
+    """Check an operand (shape None: any); returns its address.  These calls are a
+    few microseconds long on the GPU, so the checks are kept to attribute reads."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor with unit column stride (dense, or a column
     slice of a wider matrix)."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if cols > 1 and col != 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows <= 1:
         return cols
-    if t.stride(0) < cols:
+    if row < cols:
         raise ValueError(f"{name} must have a row stride of at least its {cols} columns")
-    return t.stride(0)
+    return row
 
 
-def _scratch(ws, need: int, device):
-    """(pointer, bytes) of a workspace that needs no zero-filling: the
+def _scratch(ws, need: int, like: torch.Tensor) -> tuple:
+    """(address, bytes, tensor) of a workspace that needs no zero-filling: the
     caller's, or one of this call's own."""
     if need == 0:
         return None, 0, None
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    elif isinstance(ws, Workspace):
-        ws = ws.ensure(need).buf
-    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {device}")
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+        ws = like.new_empty((need,), dtype=torch.uint8)
+    else:
+        if isinstance(ws, Workspace):
+            ws = ws.ensure(need).buf
+        if ws.get_device() != like.get_device() or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {like.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+@functools.lru_cache(maxsize=256)
+def _route_desc(top_k, score, groups, topk_groups, group_top, renormalize, scale):
+    return ctypes.byref(_Route(top_k, score, groups, topk_groups, group_top, renormalize, scale))
 
 
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -777,27 +791,36 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
     weights are the chosen scores, divided by their sum if renormalize, times
     scale.  A logit of -inf or NaN keeps its expert out; slots left without an
     expert get id -1 and weight 0."""
+    dev = _device_of(logits, "logits")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return moe_route(logits, top_k, score, bias, groups, topk_groups, group_top, renormalize, scale, weights,
+                             ids)
     if score not in _SCORES:
         raise ValueError(f"score must be one of {tuple(_SCORES)}")
-    _operand(logits, "logits", (torch.bfloat16, torch.float32), contiguous=False)
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     T, E = logits.shape
-    dev = logits.device
-    ldl = _row_stride(logits, "logits")
-    if bias is not None:
-        _operand(bias, "bias", (torch.float32,), (E,), dev)
-    r = _Route(top_k, _SCORES[score], groups, topk_groups, group_top, 1 if renormalize else 0, scale)
-    with _On(dev, stream) as s:
-        if weights is None:
-            weights = torch.empty((T, top_k if top_k > 0 else 0), dtype=torch.float32, device=dev)
-        if ids is None:
-            ids = torch.empty((T, top_k if top_k > 0 else 0), dtype=torch.int32, device=dev)
-        _operand(weights, "weights", (torch.float32,), (T, max(top_k, 0)), dev)
-        _operand(ids, "ids", (torch.int32,), (T, max(top_k, 0)), dev)
-        _check(lib().moe_route(_ptr(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, ldl, _ptr(bias),
-                               ctypes.byref(r), _ptr(weights), _ptr(ids), s), "moe_route")
+    x = _operand(logits, "logits", (torch.float32, torch.bfloat16), None, dev, contiguous=False)
+    b = None if bias is None else _operand(bias, "bias", _F32, (E,), dev)
+    out = (T, top_k if top_k > 0 else 0)
+    if weights is None:
+        weights = logits.new_empty(out, dtype=torch.float32)
+    if ids is None:
+        ids = logits.new_empty(out, dtype=torch.int32)
+    st = (_lib or lib()).moe_route(x, 0 if logits.dtype is torch.bfloat16 else 1, T, E, _row_stride(logits, "logits"),
+                                   b, _route_desc(top_k, _SCORES[score], groups, topk_groups, group_top,
+                                                  1 if renormalize else 0, scale),
+                                   _operand(weights, "weights", _F32, out, dev), _operand(ids, "ids", _I32, out, dev),
+                                   _raw_stream(dev))
+    if st:
+        _check(st, "moe_route")
     return weights, ids
+
+
+@functools.lru_cache(maxsize=1024)
+def _sort_need(pairs: int, E: int) -> int:
+    return qgd_moe_sort_workspace_size(pairs, E)
 
 
 def qgd_moe_sort_workspace_size(pairs: int, E: int) -> int:
@@ -811,22 +834,31 @@ def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=
     offsets[e + 1] - 1; order is the pair at each position (-1 behind the
     last), pos the position of each pair.  An id outside [0, E) drops its pair
     (pos -1)."""
-    _operand(ids, "ids", (torch.int32,))
-    dev, P = ids.device, ids.numel()
-    with _On(dev, stream) as s:
-        if offsets is None:
-            offsets = torch.empty((max(num_experts, 0) + 1,), dtype=torch.int32, device=dev)
-        if order is None:
-            order = torch.empty((P,), dtype=torch.int32, device=dev)
-        if pos is None:
-            pos = torch.empty_like(ids)
-        _operand(offsets, "offsets", (torch.int32,), (max(num_experts, 0) + 1,), dev)
-        _operand(order, "order", (torch.int32,), (P,), dev)
-        _operand(pos, "pos", (torch.int32,), tuple(ids.shape), dev)
-        wsp, wsn, _keep = _scratch(ws, qgd_moe_sort_workspace_size(P, num_experts), dev)
-        _check(lib().moe_sort(_ptr(ids), P, num_experts, _ptr(offsets), _ptr(order), _ptr(pos), wsp, wsn, s),
-               "moe_sort")
+    dev = _device_of(ids, "ids")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return moe_sort(ids, num_experts, offsets, order, pos, ws)
+    at = _operand(ids, "ids", _I32, None, dev)
+    P = ids.numel()
+    n_off = (num_experts + 1 if num_experts > 0 else 1,)
+    if offsets is None:
+        offsets = ids.new_empty(n_off)
+    if order is None:
+        order = ids.new_empty((P,))
+    if pos is None:
+        pos = ids.new_empty(ids.shape)
+    wsp, wsn, _keep = _scratch(ws, _sort_need(P, num_experts), ids)
+    st = (_lib or lib()).moe_sort(at, P, num_experts, _operand(offsets, "offsets", _I32, n_off, dev),
+                                  _operand(order, "order", _I32, (P,), dev),
+                                  _operand(pos, "pos", _I32, ids.shape, dev), wsp, wsn, _raw_stream(dev))
+    if st:
+        _check(st, "moe_sort")
     return offsets, order, pos
+
+
+@functools.lru_cache(maxsize=1024)
+def _experts_need(device: int, fmt: int, rows: int, E: int, N: int, K: int, act: int) -> int:
+    return qgd_experts_workspace_size(fmt, rows, E, N, K, act)
 
 
 def qgd_experts_workspace_size(fmt: int, rows: int, E: int, N: int, K: int, act: int = ACT_NONE) -> int:
@@ -845,35 +877,37 @@ def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None,
     order[i] // top_k, or row i where order is None.  x [*, K] bf16 may be a
     column slice of a wider matrix.  Rows of y behind the last expert's are
     left as they were."""
-    if act not in (ACT_NONE, ACT_SILU_MUL):
+    dev = _device_of(x, "x")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return qlinear_experts_bf16(fmt, x, wq, sw, offsets, order, top_k, act, y, ws)
+    if act != ACT_NONE and act != ACT_SILU_MUL:
         raise ValueError("act must be ACT_NONE or ACT_SILU_MUL")
-    _operand(x, "x", (torch.bfloat16,), contiguous=False)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
+    xp = _operand(x, "x", _BF16, None, dev, contiguous=False)
     x_rows, K = x.shape
-    ldx = _row_stride(x, "x")
-    dev = x.device
-    _operand(wq, "wq", (torch.int8,) if fmt == FMT_W8A8_INT8 else (torch.uint8, torch.float8_e4m3fn), device=dev)
+    wp = _operand(wq, "wq", (torch.int8,) if fmt == FMT_W8A8_INT8 else (torch.float8_e4m3fn, torch.uint8), None, dev)
     if wq.dim() != 3 or wq.shape[2] != K:
         raise ValueError(f"wq must be [experts, rows, K={K}], got {tuple(wq.shape)}")
-    E, n_all = wq.shape[0], wq.shape[1]
-    if act == ACT_SILU_MUL and n_all % 2:
+    E, n_all, _ = wq.shape
+    if act and n_all % 2:
         raise ValueError("wq must hold as many up rows as gate rows")
-    N = n_all // 2 if act == ACT_SILU_MUL else n_all
-    _operand(sw, "sw", (torch.float32,), (E, n_all), dev)
-    _operand(offsets, "offsets", (torch.int32,), (E + 1,), dev)
-    rows = x_rows
+    N = n_all // 2 if act else n_all
+    rows, op = x_rows, None
     if order is not None:
-        _operand(order, "order", (torch.int32,), device=dev)
+        op = _operand(order, "order", _I32, None, dev)
         rows = order.numel()
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
-        _operand(y, "y", (torch.bfloat16,), (rows, N), dev)
-        wsp, wsn, _keep = _scratch(ws, qgd_experts_workspace_size(fmt, rows, E, N, K, act), dev)
-        _check(lib().qlinear_experts_bf16(fmt, _ptr(x), ldx, x_rows, _ptr(order), top_k, _ptr(offsets), E, rows,
-                                          _ptr(wq), _ptr(sw), _ptr(y), N, K, act, wsp, wsn, s),
-               "qlinear_experts_bf16")
+    if y is None:
+        y = x.new_empty((rows, N))
+    wsp, wsn, _keep = _scratch(ws, _experts_need(dev, fmt, rows, E, N, K, act), x)
+    st = (_lib or lib()).qlinear_experts_bf16(fmt, xp, _row_stride(x, "x"), x_rows, op, top_k,
+                                              _operand(offsets, "offsets", _I32, (E + 1,), dev), E, rows, wp,
+                                              _operand(sw, "sw", _F32, (E, n_all), dev),
+                                              _operand(y, "y", _BF16, (rows, N), dev), N, K, act, wsp, wsn,
+                                              _raw_stream(dev))
+    if st:
+        _check(st, "qlinear_experts_bf16")
     return y
 
 
@@ -882,26 +916,25 @@ def moe_combine(h: torch.Tensor, pos, weights, add=None, y=None, stream=None):
     the slots j with pos[t, j] >= 0 of weights[t, j] * h[pos[t, j]], in fp32,
     rounded once to bf16.  h bf16 [rows, H]; pos int32 and weights fp32
     [T, top_k]; add bf16 [T, H] (may be a column slice; may be y itself)."""
-    _operand(h, "h", (torch.bfloat16,))
-    if h.dim() != 2:
-        raise ValueError("h must be 2-D")
+    dev = _device_of(h, "h")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return moe_combine(h, pos, weights, add, y)
+    hp = _operand(h, "h", _BF16, None, dev)
+    pp = _operand(pos, "pos", _I32, None, dev)
+    if h.dim() != 2 or pos.dim() != 2:
+        raise ValueError("h must be [rows, H] and pos [tokens, top_k]")
     rows, H = h.shape
-    dev = h.device
-    _operand(pos, "pos", (torch.int32,), device=dev)
-    if pos.dim() != 2:
-        raise ValueError("pos must be [tokens, top_k]")
     T, k = pos.shape
-    _operand(weights, "weights", (torch.float32,), (T, k), dev)
-    lda = 0
+    ap, lda = None, 0
     if add is not None:
-        _operand(add, "add", (torch.bfloat16,), (T, H), dev, contiguous=False)
-        lda = _row_stride(add, "add")
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        _operand(y, "y", (torch.bfloat16,), (T, H), dev)
-        _check(lib().moe_combine(_ptr(h), rows, _ptr(pos), _ptr(weights), _ptr(add), lda, _ptr(y), T, k, H, s),
-               "moe_combine")
+        ap, lda = _operand(add, "add", _BF16, (T, H), dev, contiguous=False), _row_stride(add, "add")
+    if y is None:
+        y = h.new_empty((T, H))
+    st = (_lib or lib()).moe_combine(hp, rows, pp, _operand(weights, "weights", _F32, (T, k), dev), ap, lda,
+                                     _operand(y, "y", _BF16, (T, H), dev), T, k, H, _raw_stream(dev))
+    if st:
+        _check(st, "moe_combine")
     return y
 
 

@@ -1136,6 +1136,7 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   if (n_all * E >= (1LL << 30) || (static_cast<long long>(rows) / 64 + E) * ((N + 63) / 64) > (1LL << 31) - 1)
     return fail(QGD_ERR_UNSUPPORTED, "too many weight rows or tiles (rows=%d E=%d N=%d)", rows, E, N);
   if (rows == 0) return QGD_OK;
+  if (x_rows == 0) return fail(QGD_ERR_INVALID, "%d rows of an empty x", rows);
   if (!x_bf16 || !offsets || !wq || !sw || !y_bf16) return fail(QGD_ERR_INVALID, "null operand pointer");
   if (!aligned16(x_bf16) || !aligned16(wq) || !aligned16(y_bf16) || !aligned4(order) || !aligned4(offsets) ||
       !aligned4(sw))
@@ -1167,7 +1168,7 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   a.ctas = p.ctas;
   CUtensorMap tw, tx;
   if ((st = encode_experts(&tw, wq, E, N, K, gated)) != QGD_OK) return st;
-  if ((st = encode_kmajor(&tx, q, rows, K, p.tok <= 64 ? 16 : 64)) != QGD_OK) return st;
+  if ((st = encode_kmajor(&tx, q, rows, K, experts_box_rows(p.tok))) != QGD_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_experts_quant(fmt, a, static_cast<const uint16_t*>(x_bf16), ldx, x_rows, order,
                                        order ? top_k : 1, q, s, cs);

@@ -36,8 +36,13 @@ namespace {
 __device__ __forceinline__ void record_error(unsigned int code) { atomicCAS(&g_experts_error, 0u, code); }
 
 // ---------------------------------------------------------------------------
-// Quantizer: one CTA per sorted row.  Rows behind the last expert's are left
-// alone; a source row outside x reads as zeros.
+// Quantizer: one CTA per sorted row, so that the GEMM reads every tile's rows
+// as one box.  (Gathering in the GEMM was slower: four-row tensor gathers cost
+// about 80 cycles each, and 16-byte asynchronous copies by four more warps a
+// proxy fence per stage; at 8192 tokens, 8 of 64 experts, K = 4096, 2400 and
+// 1050 us against 600 for boxes.)  A row taken by k experts is coded k times,
+// from L2.  Rows behind the last expert's are left alone; a source row outside
+// x reads as zeros.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
@@ -46,14 +51,14 @@ __global__ void __launch_bounds__(kRowThreads)
     experts_quant_kernel(const uint16_t* __restrict__ x, int K, int ldx, int x_rows, const int* __restrict__ order,
                          int div, const int* __restrict__ offsets, int E, int P, uint8_t* __restrict__ q,
                          float* __restrict__ s, unsigned* __restrict__ tickets, int ntickets) {
-  __shared__ float red[33];
+  __shared__ float red[kRowThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < ntickets; i += kRowThreads) tickets[i] = 0u;
   const int row = blockIdx.x;
+  const int pair = order ? __ldg(order + row) : row;  // (beside the offset's load, not after it)
   if (row >= min(__ldg(offsets + E), P)) return;
-  const int pair = order ? __ldg(order + row) : row;
   const int src = order ? pair / div : row;
   const bool have = pair >= 0 && src < x_rows;
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(have ? src : 0) * ldx);
@@ -79,16 +84,20 @@ __global__ void __launch_bounds__(kRowThreads)
   amax = fmaxf(amax, kAmaxFloor);
   const float sc = __fdiv_rn(amax, kQType == 0 ? kE4M3Max : kInt8Max);
   if (threadIdx.x == 0) s[row] = sc;
+  const float inv = 1.f / sc;
 #pragma unroll
   for (int j = 0; j < kVPT; ++j) {
     const int idx = threadIdx.x + j * kRowThreads;
-    if (idx < nvec) qr[idx] = encode8<kQType>(v[j], sc);
+    if (idx < nvec) qr[idx] = encode8_by_reciprocal<kQType>(v[j], sc, inv);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Grouped GEMM
 // ---------------------------------------------------------------------------
+constexpr int kThreads = kGemmThreads;  // warps: 0 loads, 1 MMA, 2-5 epilogue
+constexpr int kEpiThreads = 128;
+
 struct Ctl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
@@ -99,20 +108,24 @@ struct Ctl {
   int abort_flag;
   int last_flag;
   int epi_ok;
-  int scan[8];
+  int scan[kThreads / 32];
 };
 constexpr uint32_t kCtlBytes = 512;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block too large");
-constexpr int kEpiThreads = 128;
 constexpr uint32_t kOutBytes = 2 * 16 * 256;  // two staging buffers of 16 tokens x 128 bf16
 
-// Shared-memory map of one CTA (after 1024-byte alignment):
-//   ring of `stages` x kps x (128 weight rows + kTok token rows) x 128 bytes,
-//   output staging, token scales [2][kTok], control block, expert tile prefix.
-template <int kTok, int kKps>
+// Shapes of a variant.  kTok: most tokens per tile; kPair: a CTA pair computes
+// 256 weight rows, each CTA holding 128 of them and half of the tokens.
+// Shared memory of one CTA (after 1024-byte alignment): ring of kStages x kKps
+// x (128 weight rows + kXRows token rows) x 128 bytes, output staging, token
+// scales [2][kTok], control block, running tile counts of the experts.
+template <int kTok, int kKps, bool kPair>
 struct Layout {
+  static constexpr int kXRows = kPair ? kTok / 2 : kTok;
+  static constexpr int kRound = kPair ? 32 : 16;  // tokens of a tile are rounded up to this
+  static constexpr int kBox = kXRows > 64 ? 64 : 16;  // token rows per copy
   static constexpr uint32_t kW = kSwapTileN * kTileK;
-  static constexpr uint32_t kX = kTok * kTileK;
+  static constexpr uint32_t kX = kXRows * kTileK;
   static constexpr uint32_t kStage = kKps * (kW + kX);
   static constexpr uint32_t kTail = kOutBytes + 2 * kTok * 4 + kCtlBytes + (kMaxExperts + 1) * 4;
   static constexpr int kStages0 = static_cast<int>((kSmemBudget - 1024 - kTail) / kStage);
@@ -129,11 +142,12 @@ __device__ __forceinline__ int clamp_off(int v, int P) { return v < 0 ? 0 : (v >
 
 // Tile w of the list: weight tiles fastest, then an expert's token tiles, then
 // the experts (pre[e]: token tiles of the experts before e).  An expert's rows
-// are dealt to its token tiles evenly, in multiples of 16.
-__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, int tok, int w) {
+// are dealt to its token tiles evenly, in multiples of kRound.
+template <int kRound>
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, int n_tiles, int w) {
   Tile t;
-  const int g = w / a.n_tiles;
-  t.nt = w - g * a.n_tiles;
+  const int g = w / n_tiles;
+  t.nt = w - g * n_tiles;
   int lo = 0, hi = a.E;  // pre[lo] <= g < pre[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -143,7 +157,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, i
   t.e = lo;
   const int o0 = clamp_off(__ldg(a.offsets + lo), a.P), o1 = clamp_off(__ldg(a.offsets + lo + 1), a.P);
   const int cnt = o1 - o0, tiles = pre[lo + 1] - pre[lo];
-  const int per = ((cnt + tiles - 1) / tiles + 15) & ~15;
+  const int per = ((cnt + tiles - 1) / tiles + kRound - 1) & ~(kRound - 1);
   const int j = g - pre[lo];
   t.row0 = o0 + j * per;
   t.n = min(per, cnt - j * per);
@@ -154,21 +168,21 @@ __device__ __forceinline__ int unit_owner(long long u, long long G, long long U)
   return static_cast<int>(((u + 1) * G - 1) / U);
 }
 
-// The CTA's work as a sequence of segments (tile, K units [k0, k1)).  kSplit:
-// all (tile, K unit) units dealt out in equal contiguous ranges, one per CTA,
-// so that every SM streams the same share of the weights; else whole tiles,
-// round-robin.
+// A worker's (CTA's or CTA pair's) work as a sequence of segments (tile, K
+// units [k0, k1)).  kSplit: all (tile, K unit) units dealt out in equal
+// contiguous ranges, one per worker, so that every SM streams the same share
+// of the weights; else whole tiles, round-robin.
 template <bool kSplit>
 struct Walk {
   long long u, ue;  // kSplit: units left; else: next tile and the tile count
   int nku;
-  __device__ __forceinline__ Walk(int total, int nku_, int cta, int G) : nku(nku_) {
+  __device__ __forceinline__ Walk(int total, int nku_, int worker, int G) : nku(nku_) {
     if (kSplit) {
       const long long U = static_cast<long long>(total) * nku;
-      u = static_cast<long long>(cta) * U / G;
-      ue = static_cast<long long>(cta + 1) * U / G;
+      u = static_cast<long long>(worker) * U / G;
+      ue = static_cast<long long>(worker + 1) * U / G;
     } else {
-      u = cta;
+      u = worker;
       ue = total;
     }
   }
@@ -190,26 +204,64 @@ struct Walk {
   }
 };
 
+// Barriers with warps converged first: the instructions behind them are
+// warp-wide, and a lane that comes out of a role's branch later than the rest
+// of its warp would arrive on its own.
+__device__ __forceinline__ void epi_sync() {
+  __syncwarp();
+  named_bar_sync(1, kEpiThreads);
+}
+
+__device__ __forceinline__ void pair_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+// Tensor copies completing on the mbarrier at shared address `bar` (of a pair:
+// the leader's).
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+template <bool kPair>
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int v, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(v), "l"(policy)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "l"(policy)
+        : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, uint32_t cluster_bar,
+                                              int x, int y, uint64_t policy) {
+  if constexpr (kPair) tma_load_2d_pair(dst, map, cluster_bar, x, y, policy);
+  else tma_load_2d(dst, map, bar, x, y, policy);
 }
 
 // exp(-g) overflows to infinity for very negative g, where the quotient is the
@@ -258,7 +310,7 @@ __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, con
       buf[j * 128 + q * 32 + lane] =
           __bfloat16_as_ushort(__float2bfloat16_rn((acc_value<kFmt>(r[j]) * sxs[c0 + j]) * swv));
   }
-  named_bar_sync(1, kEpiThreads);
+  epi_sync();
   constexpr int kCols = kAct ? 64 : 128;
   constexpr int kVecs = kCols / 8;  // 16-byte vectors per token
 #pragma unroll
@@ -272,13 +324,14 @@ __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, con
   }
 }
 
-template <int kFmt, int kTok, int kKps, bool kSplit, bool kAct>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-    experts_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const ExpertArgs a) {
-  using L = Layout<kTok, kKps>;
+template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, bool kAct>
+__global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tw,
+                                                              const __grid_constant__ CUtensorMap tx,
+                                                              const ExpertArgs a) {
+  using L = Layout<kTok, kKps, kPair>;
+  static_assert(!(kSplit && kPair), "pairs take whole tiles");
   constexpr bool kInt = (kFmt == kFmtINT8);
-  constexpr int kBoxTok = kTok <= 64 ? 16 : 64;  // token rows per TMA box
-  constexpr uint32_t kCols = 2 * kTok;           // TMEM: double-buffered accumulator
+  constexpr uint32_t kCols = 2 * kTok;  // TMEM: double-buffered accumulator
   constexpr int stages = L::kStages;
 
   extern __shared__ uint8_t smem_raw[];
@@ -293,6 +346,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkt = (a.K + kTileK - 1) / kTileK;
   const int nku = (nkt + kKps - 1) / kKps;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // of a pair: 0 leads (issues the MMAs)
 
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tw);
@@ -303,7 +357,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->tfull[i], 1);
-      mbar_init(&ctl->tempty[i], 4);
+      mbar_init(&ctl->tempty[i], (kPair ? 2 : 1) * (kEpiThreads / 32));
     }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
@@ -311,18 +365,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     ctl->epi_ok = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, kCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(&ctl->tmem_base, kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&ctl->tmem_base, kCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();  // offsets, codes and scales come from the kernels before
-  // token tiles of the experts before e, as a running sum in blocks of 192 experts
+  // token tiles of the experts before e, as a running sum in blocks of experts
   {
     int carry = 0;
     if (threadIdx.x == 0) pre[0] = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kGemmThreads) {
+    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
       const int e = e0 + threadIdx.x;
       int v = 0;
       if (e < a.E) {
@@ -337,7 +397,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (lane == 31) ctl->scan[warp] = v;
       __syncthreads();
       int before = carry, all = carry;
-      for (int i = 0; i < kGemmThreads / 32; ++i) {
+      for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) before += ctl->scan[i];
         all += ctl->scan[i];
       }
@@ -346,77 +406,96 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       __syncthreads();
     }
   }
-  __syncthreads();
+  if constexpr (kPair) pair_sync();  // both CTAs' barriers and tensor memory exist
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int total = pre[a.E] * a.n_tiles;
+  const int n_tiles = kPair ? (a.n_tiles + 1) / 2 : a.n_tiles;
+  const int total = pre[a.E] * n_tiles;
   const long long U = static_cast<long long>(total) * nku;
-  // CTAs with work: every one gets at least one unit (or tile)
+  // workers with work: every one gets at least one unit (or tile)
   const long long most = kSplit ? U : total;
-  const int G = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-  const int cta = blockIdx.x;
-  const bool busy = cta < G;
+  const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
+  const int G = most < workers ? static_cast<int>(most) : workers;
+  const int me = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
+  const bool busy = me < G;
   int issued = 0;
 
+  // shared::cluster addresses of the leader's barriers (this CTA's own without a pair)
+  const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : smem_u32(&ctl->full[0]);
+  const uint32_t partner_abort = kPair ? mapa_shared(smem_u32(&ctl->abort_flag), rank ^ 1u) : 0u;
+  auto fail = [&](unsigned int code) {
+    record_error(code);
+    ctl->abort_flag = 1;
+    if constexpr (kPair) st_cluster_u32(partner_abort, 1u);
+  };
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&ctl->abort_flag) != 0; };
+
   if (warp == 0) {
-    // ---------------- TMA producer ----------------
+    // ---------------- TMA producer (of a pair: both CTAs, their halves) ----------------
     if (lane == 0 && busy) {
       const uint64_t pol_w = kSplit ? policy_evict_first() : policy_evict_last();
       const uint64_t pol_x = policy_evict_last();
-      Walk<kSplit> walk(total, nku, cta, G);
+      Walk<kSplit> walk(total, nku, me, G);
       int w, k0, k1, i = 0;
       bool stop = false;
       while (!stop && walk.next(w, k0, k1, G)) {
-        const Tile t = find_tile(a, pre, kTok, w);
-        const int boxes = (t.n + kBoxTok - 1) / kBoxTok;
+        const Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+        const int wt = kPair ? t.nt * 2 + static_cast<int>(rank) : t.nt;  // this CTA's 128 weight rows
+        const int all = (t.n + L::kRound - 1) & ~(L::kRound - 1);
+        const int mine = kPair ? all / 2 : all;            // token rows in this CTA's shared memory
+        const int xrow = t.row0 + static_cast<int>(rank) * mine;
+        const int boxes = (mine + L::kBox - 1) / L::kBox;  // rows past the tile's go unused
+        const uint32_t bytes = L::kW + boxes * L::kBox * kTileK;
         for (int k = k0; k < k1; ++k, ++i) {
           const int s = i % stages;
           if (!mbar_wait(&ctl->empty[s], ((i / stages) & 1) ^ 1)) {
-            record_error(kErrWaitProducer);
-            ctl->abort_flag = 1;
+            fail(kErrWaitProducer);
             stop = true;
             break;
           }
-          if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
+          if (aborted()) {
             stop = true;
             break;
           }
           const int kt = k * kKps, ns = min(kKps, nkt - kt);
-          mbar_arrive_expect_tx(&ctl->full[s], ns * (L::kW + boxes * kBoxTok * kTileK));
+          // the leader's barrier expects both CTAs' bytes (a copy may land first)
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], (kPair ? 2 : 1) * ns * bytes);
+          const uint32_t fb = full0 + static_cast<uint32_t>(s) * 8u;
           for (int h = 0; h < ns; ++h) {
             uint8_t* wd = w_ring + (s * kKps + h) * L::kW;
             if constexpr (kAct) {
               // four boxes of 16 gate rows and the 16 up rows of the same columns
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                tma_load_4d(wd + b * 32 * kTileK, &tw, &ctl->full[s], (kt + h) * kTileK, t.nt * 64 + b * 16, 0, t.e,
-                            pol_w);
+                tma_load_4d<kPair>(wd + b * 32 * kTileK, &tw, fb, (kt + h) * kTileK, wt * 64 + b * 16, 0, t.e, pol_w);
             } else {
-              tma_load_3d(wd, &tw, &ctl->full[s], (kt + h) * kTileK, t.nt * 128, t.e, pol_w);
+              tma_load_3d<kPair>(wd, &tw, fb, (kt + h) * kTileK, wt * 128, t.e, pol_w);
             }
             uint8_t* xd = x_ring + (s * kKps + h) * L::kX;
             for (int b = 0; b < boxes; ++b)
-              tma_load_2d(xd + b * kBoxTok * kTileK, &tx, &ctl->full[s], (kt + h) * kTileK, t.row0 + b * kBoxTok,
-                          pol_x);
+              tma_load_rows<kPair>(xd + b * L::kBox * kTileK, &tx, &ctl->full[s], fb, (kt + h) * kTileK,
+                                   xrow + b * L::kBox, pol_x);
           }
           issued = i + 1;
         }
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0 && busy) {
+    // ---------------- MMA issuer (of a pair: the leader's) ----------------
+    if (lane == 0 && rank == 0 && busy) {
       const uint32_t w_base = smem_u32(w_ring), x_base = smem_u32(x_ring);
-      Walk<kSplit> walk(total, nku, cta, G);
+      Walk<kSplit> walk(total, nku, me, G);
       int w, k0, k1, i = 0, li = 0;
       bool stop = false;
       while (!stop && walk.next(w, k0, k1, G)) {
-        const Tile t = find_tile(a, pre, kTok, w);
-        const uint32_t idesc = idesc_mma(kInt ? 2 : 1, kInt ? 1 : 0, kSwapTileN, (t.n + 15) & ~15);
+        const Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+        const uint32_t idesc = idesc_mma(kInt ? 2 : 1, kInt ? 1 : 0, (kPair ? 2 : 1) * kSwapTileN,
+                                         (t.n + L::kRound - 1) & ~(L::kRound - 1));
         const int b = li & 1;
         if (!mbar_wait(&ctl->tempty[b], ((li >> 1) & 1) ^ 1)) {
-          record_error(kErrWaitMma);
-          ctl->abort_flag = 1;
+          fail(kErrWaitMma);
           break;
         }
         tc_fence_after();
@@ -424,12 +503,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int k = k0; k < k1; ++k, ++i) {
           const int s = i % stages;
           if (!mbar_wait(&ctl->full[s], (i / stages) & 1)) {
-            record_error(kErrWaitMma);
-            ctl->abort_flag = 1;
+            fail(kErrWaitMma);
             stop = true;
             break;
           }
-          if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
+          if (aborted()) {
             stop = true;
             break;
           }
@@ -440,13 +518,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int kk = 0; kk < kTileK / 32; ++kk) {
               const uint64_t ad = sdesc_kmajor_sw128(w_base + (s * kKps + h) * L::kW + kk * 32);
               const uint64_t bd = sdesc_kmajor_sw128(x_base + (s * kKps + h) * L::kX + kk * 32);
-              mma_issue<kInt>(d, ad, bd, idesc, (k > k0 || h > 0 || kk > 0) ? 1u : 0u);
+              const uint32_t acc = (k > k0 || h > 0 || kk > 0) ? 1u : 0u;
+              if constexpr (kPair) mma_issue_pair<kInt>(d, ad, bd, idesc, acc);
+              else mma_issue<kInt>(d, ad, bd, idesc, acc);
             }
           }
-          mma_commit(&ctl->empty[s]);
+          if constexpr (kPair) mma_commit_pair(&ctl->empty[s], 0x3);
+          else mma_commit(&ctl->empty[s]);
         }
         if (stop) break;
-        mma_commit(&ctl->tfull[b]);
+        if constexpr (kPair) mma_commit_pair(&ctl->tfull[b], 0x3);
+        else mma_commit(&ctl->tfull[b]);
         ++li;
       }
     }
@@ -456,11 +538,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3, et = threadIdx.x - 64;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int lrow = q * 32 + lane;  // row of the weight tile
-    Walk<kSplit> walk(total, nku, cta, G);
+    const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
+    Walk<kSplit> walk(total, nku, me, G);
     int w, k0, k1, li = 0;
     uint32_t flip = 0;
     while (walk.next(w, k0, k1, G)) {
-      const Tile t = find_tile(a, pre, kTok, w);
+      Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+      if constexpr (kPair) t.nt = t.nt * 2 + static_cast<int>(rank);
       const int b = li & 1;
       float* sxs = sx_s + b * kTok;
       for (int i = et; i < ((t.n + 15) & ~15); i += kEpiThreads) sxs[i] = i < t.n ? __ldg(a.sx + t.row0 + i) : 0.f;
@@ -474,23 +558,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * a.N + col);
       }
       const bool ok = warp_wait(&ctl->tfull[b], (li >> 1) & 1);
-      if (!ok && lane == 0) {
-        record_error(kErrWaitEpilogue);
-        ctl->abort_flag = 1;
-      }
+      if (!ok && lane == 0) fail(kErrWaitEpilogue);
       if (ok) tc_fence_after();
-      named_bar_sync(1, kEpiThreads);
-      if (et == 0) ctl->epi_ok = (*reinterpret_cast<volatile int*>(&ctl->abort_flag) == 0);
-      named_bar_sync(1, kEpiThreads);
+      epi_sync();
+      if (et == 0) ctl->epi_ok = !aborted();
+      epi_sync();
       if (!ctl->epi_ok) break;
       const bool whole = !kSplit || (k0 == 0 && k1 == nku);
-      int first = cta, ncontrib = 1;
+      int first = me, ncontrib = 1;
       uint32_t* slot = nullptr;
       if (!whole) {
         const long long u0 = static_cast<long long>(w) * nku;
         first = unit_owner(u0, G, U);
         ncontrib = unit_owner(u0 + nku - 1, G, U) - first + 1;
-        slot = a.partial + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * (kSwapTileN * kTok) + lrow;
+        slot = a.partial + (static_cast<size_t>(me) * 2 + (me == first ? 1 : 0)) * (kSwapTileN * kTok) + lrow;
       }
       const int chunks = (t.n + 15) >> 4;
       for (int c = 0; c < chunks; ++c) {
@@ -501,7 +582,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (c == chunks - 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->tempty[b]);
+          if (lane == 0) {
+            if constexpr (kPair) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(b) * 8u);
+            else mbar_arrive(&ctl->tempty[b]);
+          }
         }
         if (whole) {
           finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, flip);
@@ -512,13 +596,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (!whole) {
         // the last of the tile's CTAs to arrive adds the partials in CTA order
-        named_bar_sync(1, kEpiThreads);
+        epi_sync();
         if (et == 0) {
           unsigned old;
           asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.tickets + first) : "memory");
           ctl->last_flag = (old == static_cast<unsigned>(ncontrib - 1));
         }
-        named_bar_sync(1, kEpiThreads);
+        epi_sync();
         if (ctl->last_flag) {
           for (int c = 0; c < chunks; ++c) {
             uint32_t sum[16];
@@ -540,27 +624,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 
   // ---------------- teardown ----------------
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
-  if (ctl->abort_flag) {
+  // one answer for every thread (a partner may set the flag at any time)
+  if (__syncthreads_or(ctl->abort_flag != 0)) {
     if (warp == 0 && lane == 0) {
-      // the last copies issued into each stage must land before the CTA exits
-      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
-        if (!mbar_wait(&ctl->full[i % stages], (i / stages) & 1)) {
-          record_error(kErrWaitDrain);
-          break;
+      // the last copies issued into each stage (both CTAs') must land before either CTA exits
+      if (rank == 0)
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
+          if (!mbar_wait(&ctl->full[i % stages], (i / stages) & 1)) {
+            record_error(kErrWaitDrain);
+            break;
+          }
         }
-      }
     }
-    if (warp == 1 && lane == 0) {
-      mma_commit(&ctl->drain);
+    if (rank == 0 && warp == 1 && lane == 0) {
+      if constexpr (kPair) mma_commit_pair(&ctl->drain, 0x1);
+      else mma_commit(&ctl->drain);
       if (!mbar_wait(&ctl->drain, 0)) record_error(kErrWaitDrain);
     }
     __syncthreads();
   }
+  if constexpr (kPair) pair_sync();  // neither CTA leaves while its partner may still signal its barriers
+  __syncwarp();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    if constexpr (kPair) tmem_dealloc_pair(tmem, kCols);
+    else tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -597,24 +687,69 @@ cudaError_t launch_quant_t(const ExpertArgs& a, const uint16_t* x, int ldx, int 
   return cudaErrorInvalidValue;
 }
 
-template <int kFmt, int kTok, int kKps, bool kSplit, bool kAct>
+template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, bool kAct>
 cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a, cudaStream_t st) {
-  using L = Layout<kTok, kKps>;
+  using L = Layout<kTok, kKps, kPair>;
   static_assert(L::kStages >= 2 && L::kBytes <= kSmemBudget, "ring does not fit");
-  auto kernel = experts_kernel<kFmt, kTok, kKps, kSplit, kAct>;
+  // more than half an SM's shared memory, so that no two of these CTAs, which
+  // may take all tensor-memory columns, share an SM
+  static_assert(L::kBytes > kSmemPerSM / 2, "two CTAs would fit");
+  auto kernel = experts_kernel<kFmt, kTok, kKps, kSplit, kPair, kAct>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, L::kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(a.ctas), dim3(kGemmThreads), L::kBytes, st, tw, tx, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if constexpr (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+    // no more pairs than fit on the GPU at once: the tiles are dealt out over
+    // the grid, so a pair that had to wait for a place would end last
+    static std::atomic<int> fit[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int pairs = fit[dev & 63].load(std::memory_order_relaxed);
+    cfg.gridDim = dim3(a.ctas & ~1);
+    if (pairs == 0) {
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) {
+        (void)cudaGetLastError();
+        pairs = a.ctas / 2;
+      }
+      fit[dev & 63].store(pairs, std::memory_order_relaxed);
+    }
+    if (a.ctas / 2 > pairs) cfg.gridDim = dim3(2 * pairs);
+  }
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int kFmt, bool kAct>
 cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a, cudaStream_t st) {
-  return a.tok <= 64 ? launch_t<kFmt, 64, 2, true, kAct>(tw, tx, a, st)
-                     : launch_t<kFmt, 256, 1, false, kAct>(tw, tx, a, st);
+  return a.tok <= 64 ? launch_t<kFmt, 64, 2, true, false, kAct>(tw, tx, a, st)
+                     : launch_t<kFmt, 256, 1, false, true, kAct>(tw, tx, a, st);
 }
 
 }  // namespace
+
+int experts_box_rows(int tok) { return tok <= 64 ? Layout<64, 2, false>::kBox : Layout<256, 1, true>::kBox; }
 
 cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
                                  const int* order, int div, uint8_t* q, float* s, cudaStream_t stream) {

@@ -256,6 +256,48 @@ def test_experts_bad_offsets_and_rows_stay_in_bounds():
     moelib.close(y, ref, moelib.experts_tolerance(ref, mag, K, False, True))
 
 
+def _awkward_rows(rows, K, qmax, seed):
+    """bf16 rows whose quotients by the row scale crowd around the codes'
+    rounding boundaries, with zeros, subnormals, infinities and NaNs."""
+    g = _gen(seed)
+    x = torch.randn((rows, K), generator=g).double()
+    amax = torch.exp2(torch.randint(-30, 30, (rows, 1), generator=g).double()) * (1 + torch.rand((rows, 1), generator=g))
+    amax = amax.bfloat16().double()
+    step = amax / qmax
+    half = torch.randint(0, 2 * int(qmax), (rows, K), generator=g).double() + 0.5
+    near = half * step * 0.5 * torch.where(torch.rand((rows, K), generator=g) < 0.5, 1.0, -1.0)
+    fine = step * torch.exp2(-torch.randint(0, 12, (rows, K), generator=g).double()) * torch.randint(1, 16, (rows, K), generator=g)
+    pick = torch.rand((rows, K), generator=g)
+    x = torch.where(pick < 0.5, near, torch.where(pick < 0.9, fine, x * step))
+    x = torch.where(x.abs() > amax, amax, x).bfloat16()
+    x[:, 0] = amax[:, 0].bfloat16()
+    x[0] = 0
+    x[1, :] = 1e-40
+    x[2, 3], x[2, 4] = float("inf"), float("-inf")
+    x[3, 5] = float("nan")
+    x[4] = -0.0
+    x[4, 7] = 3e38
+    return x
+
+
+@pytest.mark.parametrize("fmt,qmax", [("w8a8_int8", 127.0), ("fp8_dynamic", 448.0)])
+@pytest.mark.parametrize("rows", [48, 700])
+def test_experts_same_bits_as_the_dense_layer(fmt, qmax, rows):
+    # unit weights give back the codes: they have to be the dense quantizer's, bit for bit
+    K = 1024
+    int8 = fmt == "w8a8_int8"
+    fid = qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC
+    x = _awkward_rows(rows, K, qmax, 17).cuda()
+    one = 1 if int8 else 0x38  # e4m3 1.0
+    wq = (torch.eye(K) * one).to(torch.int8 if int8 else torch.uint8).cuda()
+    sw = torch.ones(K, device="cuda")
+    dense = qgd.qlinear_bf16(fid, x, wq, sw)
+    off = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+    y = qgd.qlinear_experts_bf16(fid, x, torch.stack([wq, wq]), torch.stack([sw, sw]), off)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), dense.view(torch.int16))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
