@@ -398,8 +398,9 @@ QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int*
  * Offsets are read on the device, clamped to [0, rows]; a source row outside
  * [0, x_rows) counts as zeros.  N % 16 == 0; K % 16 == 0, K <= 16384;
  * 1 <= E <= QGD_MAX_EXPERTS.  x, wq, y and ws 16-byte aligned.  y must not
- * overlap the inputs. */
-QGD_API size_t qgd_experts_workspace_size(int fmt, int rows, int E, int N, int K, int act);
+ * overlap the inputs.  Workspace: qgd_experts_workspace_size() bytes, its
+ * x_rows 0 for a call without an order. */
+QGD_API size_t qgd_experts_workspace_size(int fmt, int rows, int x_rows, int E, int N, int K, int act);
 QGD_API qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows, const int* order, int top_k,
                                         const int* offsets, int E, int rows, const void* wq, const float* sw,
                                         void* y_bf16, int N, int K, int act, void* ws, size_t ws_bytes, void* stream);

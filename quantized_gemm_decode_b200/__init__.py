@@ -160,7 +160,7 @@ def lib() -> ctypes.CDLL:
         L.qgd_tp_workspace_size.restype = S
         L.qgd_moe_sort_workspace_size.argtypes = [I, I]
         L.qgd_moe_sort_workspace_size.restype = S
-        L.qgd_experts_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.qgd_experts_workspace_size.argtypes = [I, I, I, I, I, I, I]
         L.qgd_experts_workspace_size.restype = S
         L.qgd_m_bucket.argtypes = [I]
         L.qgd_m_bucket.restype = I
@@ -857,12 +857,13 @@ def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=
 
 
 @functools.lru_cache(maxsize=1024)
-def _experts_need(device: int, fmt: int, rows: int, E: int, N: int, K: int, act: int) -> int:
-    return qgd_experts_workspace_size(fmt, rows, E, N, K, act)
+def _experts_need(device: int, fmt: int, rows: int, x_rows: int, E: int, N: int, K: int, act: int) -> int:
+    return qgd_experts_workspace_size(fmt, rows, x_rows, E, N, K, act)
 
 
-def qgd_experts_workspace_size(fmt: int, rows: int, E: int, N: int, K: int, act: int = ACT_NONE) -> int:
-    return int(lib().qgd_experts_workspace_size(fmt, rows, E, N, K, act))
+def qgd_experts_workspace_size(fmt: int, rows: int, x_rows: int, E: int, N: int, K: int, act: int = ACT_NONE) -> int:
+    """Workspace bytes of a qlinear_experts_bf16 call; x_rows is 0 for a call without an order."""
+    return int(lib().qgd_experts_workspace_size(fmt, rows, x_rows, E, N, K, act))
 
 
 def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None, top_k: int = 1,
@@ -900,7 +901,7 @@ def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None,
         rows = order.numel()
     if y is None:
         y = x.new_empty((rows, N))
-    wsp, wsn, _keep = _scratch(ws, _experts_need(dev, fmt, rows, E, N, K, act), x)
+    wsp, wsn, _keep = _scratch(ws, _experts_need(dev, fmt, rows, 0 if op is None else x_rows, E, N, K, act), x)
     st = (_lib or lib()).qlinear_experts_bf16(fmt, xp, _row_stride(x, "x"), x_rows, op, top_k,
                                               _operand(offsets, "offsets", _I32, (E + 1,), dev), E, rows, wp,
                                               _operand(sw, "sw", _F32, (E, n_all), dev),

@@ -737,10 +737,12 @@ constexpr int kMaxExpertCtas = 256;  // SMs of any sm_100 part
 
 struct ExpertPlan {
   int tok = 0, n_tiles = 0, ctas = 0;
-  size_t q_off = 0, s_off = 0, part_off = 0, total = 0;
+  bool code_once = false;  // code each row of x once and copy the codes into sorted order
+  size_t q_off = 0, s_off = 0, part_off = 0, q0_off = 0, s0_off = 0, total = 0;
 };
 
-ExpertPlan expert_plan(int rows, int E, int N, int K, bool act) {
+// x_rows: rows of x behind an order, or 0 without one
+ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
   ExpertPlan p;
   // few rows per expert: 64-token tiles whose K range is shared out over all
   // SMs (weights streamed once bound them); many: 256-token tiles
@@ -751,17 +753,24 @@ ExpertPlan expert_plan(int rows, int E, int N, int K, bool act) {
   p.s_off = align256(p.q_off + static_cast<size_t>(rows) * K);
   p.part_off = align256(p.s_off + static_cast<size_t>(rows) * 4);
   p.total = p.part_off + (p.tok <= 64 ? static_cast<size_t>(p.ctas) * 2 * p.tok * kSwapTileN * 4 : 0);
+  // (16 M codes: where the second launch costs less than coding again)
+  p.code_once = x_rows > 0 && rows >= 2 * static_cast<long long>(x_rows) && static_cast<long long>(rows) * K >= (1LL << 24);
+  if (p.code_once) {
+    p.q0_off = align256(p.total);
+    p.s0_off = align256(p.q0_off + static_cast<size_t>(x_rows) * K);
+    p.total = align256(p.s0_off + static_cast<size_t>(x_rows) * 4);
+  }
   return p;
 }
 
 // Expert weights [E][rows][K] as boxes of 128 bytes x 128 rows, or with the
-// gated activation [E][2][N][K] as 128 bytes x 16 gate rows and their 16 up
+// gated activation [E][2][N][K] as 128 bytes x 64 gate rows and their 64 up
 // rows; 128-byte swizzle, zeros past the extents.
 qgd_status encode_experts(CUtensorMap* map, const void* base, int E, int N, int K, bool act) {
   const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), e = static_cast<cuuint64_t>(E);
   cuuint64_t dims[4] = {k, n, act ? 2 : e, e};
   cuuint64_t strides[3] = {k, k * n, 2 * k * n};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(kTileK), act ? 16u : 128u, act ? 2u : 1u, 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(kTileK), act ? 64u : 128u, act ? 2u : 1u, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, act ? 4 : 3, const_cast<void*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1108,12 +1117,12 @@ qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, 
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_sort launch");
 }
 
-size_t qgd_experts_workspace_size(int fmt, int rows, int E, int N, int K, int act) {
-  if ((fmt != kFmtFP8 && fmt != kFmtINT8) || rows <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
+size_t qgd_experts_workspace_size(int fmt, int rows, int x_rows, int E, int N, int K, int act) {
+  if ((fmt != kFmtFP8 && fmt != kFmtINT8) || rows <= 0 || x_rows < 0 || E <= 0 || N <= 0 || K <= 0) return 0;
   int devices = 0;  // on a GPU host the plan follows the device's SM count, as in the call
   if (cudaGetDeviceCount(&devices) == cudaSuccess && devices > 0) (void)check_device();
   else (void)cudaGetLastError();
-  return expert_plan(rows, E, N, K, act == QGD_ACT_SILU_MUL).total;
+  return expert_plan(rows, x_rows, E, N, K, act == QGD_ACT_SILU_MUL).total;
 }
 
 qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows, const int* order, int top_k,
@@ -1145,7 +1154,7 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   if ((st = check_device()) != QGD_OK) return st;
   if ((st = get_encoder()) != QGD_OK) return st;
   const bool gated = act == QGD_ACT_SILU_MUL;
-  const ExpertPlan p = expert_plan(rows, E, N, K, gated);
+  const ExpertPlan p = expert_plan(rows, order ? x_rows : 0, E, N, K, gated);
   if (!ws || ws_bytes < p.total)
     return fail(QGD_ERR_WORKSPACE, "experts workspace of %zu bytes needed, %zu given", p.total, ws ? ws_bytes : 0);
   if (!aligned16(ws)) return fail(QGD_ERR_INVALID, "workspace must be 16-byte aligned");
@@ -1166,14 +1175,16 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   a.n_tiles = p.n_tiles;
   a.tok = p.tok;
   a.ctas = p.ctas;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx, tx_short;
   if ((st = encode_experts(&tw, wq, E, N, K, gated)) != QGD_OK) return st;
-  if ((st = encode_kmajor(&tx, q, rows, K, experts_box_rows(p.tok))) != QGD_OK) return st;
+  if ((st = encode_kmajor(&tx, q, rows, K, experts_box_rows(p.tok, false))) != QGD_OK) return st;
+  if ((st = encode_kmajor(&tx_short, q, rows, K, experts_box_rows(p.tok, true))) != QGD_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_experts_quant(fmt, a, static_cast<const uint16_t*>(x_bf16), ldx, x_rows, order,
-                                       order ? top_k : 1, q, s, cs);
+                                       order ? top_k : 1, q, s, p.code_once ? wsb + p.q0_off : nullptr,
+                                       reinterpret_cast<float*>(wsb + p.s0_off), cs);
   if (e != cudaSuccess) return cuda_fail(e, "experts quantizer launch");
-  e = launch_experts(fmt, gated, tw, tx, a, cs);
+  e = launch_experts(fmt, gated, tw, tx, tx_short, a, cs);
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "grouped GEMM launch");
 }
 

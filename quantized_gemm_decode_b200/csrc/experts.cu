@@ -8,15 +8,15 @@
 //     y[i][n] = bf16(v[n]), or with the gated activation over 2N weight rows
 //               bf16(silu(v[n]) * v[N + n]),  silu(g) = g / (1 + exp(-g))
 //
-// Two kernels: the quantizer writes the codes in sorted order, then one
-// persistent kernel walks the (expert, token tile, weight tile) tiles, whose
+// The quantizer writes the codes in sorted order, then one persistent kernel walks the (expert, token tile, weight tile) tiles, whose
 // number only the device knows, from the offsets.  Orientation as in the
 // dense decode kernel (weights in the MMA's 128-row M slot, tokens in its N),
 // because an expert's row count is ragged: N follows the tile's rows in steps
 // of 16, where M would round every expert up to 128.
 //
-// Warp roles (192 threads): warp 0 issues TMA loads, warp 1 owns TMEM and
-// issues MMAs, warps 2-5 drain the accumulator.  Every wait is bounded.
+// Warp roles: warp 0 issues TMA loads, warp 1 owns TMEM and
+// issues MMAs, the groups of four warps behind them drain the accumulator.
+// Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -40,9 +40,8 @@ __device__ __forceinline__ void record_error(unsigned int code) { atomicCAS(&g_e
 // as one box.  (Gathering in the GEMM was slower: four-row tensor gathers cost
 // about 80 cycles each, and 16-byte asynchronous copies by four more warps a
 // proxy fence per stage; at 8192 tokens, 8 of 64 experts, K = 4096, 2400 and
-// 1050 us against 600 for boxes.)  A row taken by k experts is coded k times,
-// from L2.  Rows behind the last expert's are left alone; a source row outside
-// x reads as zeros.
+// 1050 us against 600 for boxes.)  Rows behind the last expert's are left
+// alone; a source row outside x reads as zeros.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
@@ -58,7 +57,7 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int i = threadIdx.x; i < ntickets; i += kRowThreads) tickets[i] = 0u;
   const int row = blockIdx.x;
   const int pair = order ? __ldg(order + row) : row;  // (beside the offset's load, not after it)
-  if (row >= min(__ldg(offsets + E), P)) return;
+  if (offsets && row >= min(__ldg(offsets + E), P)) return;
   const int src = order ? pair / div : row;
   const bool have = pair >= 0 && src < x_rows;
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(have ? src : 0) * ldx);
@@ -92,11 +91,44 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// Many rows that several experts take: each row of x is coded once and the
+// codes are copied into sorted order, a warp per row.  Coding costs about 20
+// issue slots a value, so coding k times is bound by the SMs (181 us for 65536
+// rows of 4096, 8 per row of x) where the copy is bound by its stores.
+constexpr int kPermuteThreads = 256;
+
+__global__ void __launch_bounds__(kPermuteThreads)
+    permute_codes_kernel(const uint4* __restrict__ q0, const float* __restrict__ s0, int x_rows,
+                         const int* __restrict__ order, int div, const int* __restrict__ offsets, int E, int P, int nvec,
+                         uint4* __restrict__ q, float* __restrict__ s) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * (kPermuteThreads / 32) + (threadIdx.x >> 5);
+  if (row >= P) return;
+  const int pair = __ldg(order + row);
+  if (row >= __ldg(offsets + E)) return;
+  const int src = pair / div;
+  const bool have = pair >= 0 && src < x_rows;
+  const uint4* from = q0 + static_cast<size_t>(have ? src : 0) * nvec;
+  uint4* to = q + static_cast<size_t>(row) * nvec;
+  for (int v0 = lane; v0 < nvec; v0 += 8 * 32) {
+    uint4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v0 + j * 32 < nvec) v[j] = have ? __ldg(from + v0 + j * 32) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v0 + j * 32 < nvec) to[v0 + j * 32] = v[j];
+  }
+  if (lane == 0) s[row] = have ? __ldg(s0 + src) : 0.f;
+}
+
 // ---------------------------------------------------------------------------
 // Grouped GEMM
 // ---------------------------------------------------------------------------
-constexpr int kThreads = kGemmThreads;  // warps: 0 loads, 1 MMA, 2-5 epilogue
-constexpr int kEpiThreads = 128;
+constexpr int kEpiThreads = 128;  // an epilogue group: four warps, one per quarter of the tensor-memory lanes
+constexpr int kMaxWarps = 2 + 4 * 4;
 
 struct Ctl {
   uint64_t full[kMaxStages];
@@ -107,27 +139,35 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   int last_flag;
-  int epi_ok;
-  int scan[kThreads / 32];
+  int epi_ok[4];
+  int scan[kMaxWarps];
 };
 constexpr uint32_t kCtlBytes = 512;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block too large");
-constexpr uint32_t kOutBytes = 2 * 16 * 256;  // two staging buffers of 16 tokens x 128 bf16
 
 // Shapes of a variant.  kTok: most tokens per tile; kPair: a CTA pair computes
-// 256 weight rows, each CTA holding 128 of them and half of the tokens.
+// 256 weight rows, each CTA holding 128 of them and half of the tokens;
+// kGroups: epilogue groups, which take a tile's 16-token chunks in turn.
 // Shared memory of one CTA (after 1024-byte alignment): ring of kStages x kKps
-// x (128 weight rows + kXRows token rows) x 128 bytes, output staging, token
-// scales [2][kTok], control block, running tile counts of the experts.
-template <int kTok, int kKps, bool kPair>
+// x (128 weight rows + kXRows token rows) x 128 bytes; per epilogue group two
+// output staging buffers of 16 tokens x 128 bf16 (with the activation an
+// exchange area of 8 x 128 floats and one buffer of 16 x 64) and the token
+// scales [2][kTok]; control block; running tile counts of the experts.
+template <int kTok, int kKps, bool kPair, int kGroups, bool kAct>
 struct Layout {
+  static constexpr int kThreads = 64 + kGroups * kEpiThreads;
+  static constexpr uint32_t kOut = kAct ? 8 * kEpiThreads * 4 + 16 * 128 : 2 * 16 * 256;
+  static constexpr uint32_t kGroupBytes = kOut + 2 * kTok * 4;
   static constexpr int kXRows = kPair ? kTok / 2 : kTok;
   static constexpr int kRound = kPair ? 32 : 16;  // tokens of a tile are rounded up to this
-  static constexpr int kBox = kXRows > 64 ? 64 : 16;  // token rows per copy
+  // token rows per copy: few for short tiles, all for long ones (a copy costs
+  // the copy engine about 150 cycles whatever its size, a K slice of a full
+  // pair tile about 750 cycles of MMA)
+  static constexpr int kBoxShort = kXRows / 4, kBoxLong = kXRows;
   static constexpr uint32_t kW = kSwapTileN * kTileK;
   static constexpr uint32_t kX = kXRows * kTileK;
   static constexpr uint32_t kStage = kKps * (kW + kX);
-  static constexpr uint32_t kTail = kOutBytes + 2 * kTok * 4 + kCtlBytes + (kMaxExperts + 1) * 4;
+  static constexpr uint32_t kTail = kGroups * kGroupBytes + kCtlBytes + (kMaxExperts + 1) * 4;
   static constexpr int kStages0 = static_cast<int>((kSmemBudget - 1024 - kTail) / kStage);
   static constexpr int kStages = kStages0 > kMaxStages ? kMaxStages : kStages0;
   static constexpr size_t kBytes = 1024 + static_cast<size_t>(kStages) * kStage + kTail;
@@ -207,9 +247,9 @@ struct Walk {
 // Barriers with warps converged first: the instructions behind them are
 // warp-wide, and a lane that comes out of a role's branch later than the rest
 // of its warp would arrive on its own.
-__device__ __forceinline__ void epi_sync() {
+__device__ __forceinline__ void epi_sync(int group) {
   __syncwarp();
-  named_bar_sync(1, kEpiThreads);
+  named_bar_sync(1 + group, kEpiThreads);
 }
 
 __device__ __forceinline__ void pair_sync() {
@@ -281,36 +321,50 @@ __device__ __forceinline__ uint32_t add_acc(uint32_t x, uint32_t y) {
 }
 
 // Sixteen tokens of this thread's weight row, finished and stored.  r: the
-// accumulators of tokens c0 .. c0 + 15 of the tile.  The epilogue warps write
+// accumulators of tokens c0 .. c0 + 15 of the tile.  The group's warps write
 // bf16 rows [token][column] to shared memory and then store whole 16-byte
 // vectors, so that y leaves in 128- or 256-byte runs although a thread holds
-// one column.  With the activation a warp holds 16 gate rows (lanes 0-15) and
-// their 16 up rows (lanes 16-31): each pair of lanes swaps halves, the lower
-// lane finishes the even tokens, the upper one the odd ones.
+// one column.  With the activation the first two warps hold 64 gate rows and
+// the last two their up rows: two threads of one column swap halves through
+// shared memory, the gate's finishing the even tokens, the up's the odd ones.
+// `out`: exchange area (activation only) and staging, see Layout.  Without the
+// activation staging alternates between two buffers; with it the exchange's
+// barrier already keeps a chunk's stores ahead of the next chunk's values.
 template <int kFmt, bool kAct>
 __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, const uint32_t (&r)[16], int c0, float swv,
-                                         const float* sxs, uint8_t* out, uint32_t& flip) {
-  const int et = threadIdx.x - 64, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3;
-  uint16_t* buf = reinterpret_cast<uint16_t*>(out + (flip & 1u) * (16 * 256));
-  flip ^= 1u;
+                                         const float* sxs, uint8_t* out, int group, uint32_t& flip) {
+  const int et = (threadIdx.x - 64) & (kEpiThreads - 1), lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 f = *reinterpret_cast<const float4*>(sxs + c0 + 4 * j);
+    v[4 * j] = (acc_value<kFmt>(r[4 * j]) * f.x) * swv;
+    v[4 * j + 1] = (acc_value<kFmt>(r[4 * j + 1]) * f.y) * swv;
+    v[4 * j + 2] = (acc_value<kFmt>(r[4 * j + 2]) * f.z) * swv;
+    v[4 * j + 3] = (acc_value<kFmt>(r[4 * j + 3]) * f.w) * swv;
+  }
+  uint16_t* buf;
   if constexpr (kAct) {
-    const bool up = lane >= 16;
+    float* swap = reinterpret_cast<float*>(out);
+    buf = reinterpret_cast<uint16_t*>(out + 8 * kEpiThreads * 4);
+    const bool up = q >= 2;
+    const int row = q * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) swap[j * kEpiThreads + row] = up ? v[2 * j] : v[2 * j + 1];
+    epi_sync(group);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float even = (acc_value<kFmt>(r[2 * j]) * sxs[c0 + 2 * j]) * swv;
-      const float odd = (acc_value<kFmt>(r[2 * j + 1]) * sxs[c0 + 2 * j + 1]) * swv;
-      const float other = __shfl_xor_sync(0xffffffffu, up ? even : odd, 16);
-      const float gate = up ? other : even, lin = up ? odd : other;
-      buf[(2 * j + (up ? 1 : 0)) * 64 + q * 16 + (lane & 15)] =
-          __bfloat16_as_ushort(__float2bfloat16_rn(silu(gate) * lin));
+      const float other = swap[j * kEpiThreads + (row ^ 64)];
+      const float gate = up ? other : v[2 * j], lin = up ? v[2 * j + 1] : other;
+      buf[(2 * j + (up ? 1 : 0)) * 64 + (row & 63)] = __bfloat16_as_ushort(__float2bfloat16_rn(silu(gate) * lin));
     }
   } else {
+    buf = reinterpret_cast<uint16_t*>(out + (flip & 1u) * (16 * 256));
+    flip ^= 1u;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      buf[j * 128 + q * 32 + lane] =
-          __bfloat16_as_ushort(__float2bfloat16_rn((acc_value<kFmt>(r[j]) * sxs[c0 + j]) * swv));
+    for (int j = 0; j < 16; ++j) buf[j * 128 + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
   }
-  epi_sync();
+  epi_sync(group);
   constexpr int kCols = kAct ? 64 : 128;
   constexpr int kVecs = kCols / 8;  // 16-byte vectors per token
 #pragma unroll
@@ -324,12 +378,13 @@ __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, con
   }
 }
 
-template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, bool kAct>
-__global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tw,
-                                                              const __grid_constant__ CUtensorMap tx,
-                                                              const ExpertArgs a) {
-  using L = Layout<kTok, kKps, kPair>;
-  static_assert(!(kSplit && kPair), "pairs take whole tiles");
+template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, int kGroups, bool kAct>
+__global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThreads, 1)
+    experts_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+                   const __grid_constant__ CUtensorMap tx_short, const ExpertArgs a) {
+  using L = Layout<kTok, kKps, kPair, kGroups, kAct>;
+  constexpr int kThreads = L::kThreads;
+  static_assert(!kSplit || (!kPair && kGroups == 1), "tiles are split between single CTAs with one epilogue group");
   constexpr bool kInt = (kFmt == kFmtINT8);
   constexpr uint32_t kCols = 2 * kTok;  // TMEM: double-buffered accumulator
   constexpr int stages = L::kStages;
@@ -338,9 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   uint8_t* base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   uint8_t* w_ring = base;
   uint8_t* x_ring = base + stages * kKps * L::kW;
-  uint8_t* out = base + stages * L::kStage;
-  float* sx_s = reinterpret_cast<float*>(out + kOutBytes);
-  Ctl* ctl = reinterpret_cast<Ctl*>(sx_s + 2 * kTok);
+  uint8_t* groups = base + stages * L::kStage;
+  Ctl* ctl = reinterpret_cast<Ctl*>(groups + kGroups * L::kGroupBytes);
   int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + kCtlBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -351,18 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tw);
     tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tx_short);
     for (int i = 0; i < stages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->tfull[i], 1);
-      mbar_init(&ctl->tempty[i], (kPair ? 2 : 1) * (kEpiThreads / 32));
+      mbar_init(&ctl->tempty[i], (kPair ? 2 : 1) * kGroups * (kEpiThreads / 32));
     }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     ctl->last_flag = 0;
-    ctl->epi_ok = 0;
     fence_mbar_init();
   }
   __syncwarp();
@@ -445,8 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         const int all = (t.n + L::kRound - 1) & ~(L::kRound - 1);
         const int mine = kPair ? all / 2 : all;            // token rows in this CTA's shared memory
         const int xrow = t.row0 + static_cast<int>(rank) * mine;
-        const int boxes = (mine + L::kBox - 1) / L::kBox;  // rows past the tile's go unused
-        const uint32_t bytes = L::kW + boxes * L::kBox * kTileK;
+        // rows past the tile's go unused
+        const bool few = mine <= L::kBoxShort;
+        const CUtensorMap* xmap = few ? &tx_short : &tx;
+        const uint32_t bytes = L::kW + (few ? L::kBoxShort : L::kBoxLong) * kTileK;
         for (int k = k0; k < k1; ++k, ++i) {
           const int s = i % stages;
           if (!mbar_wait(&ctl->empty[s], ((i / stages) & 1) ^ 1)) {
@@ -465,17 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
           for (int h = 0; h < ns; ++h) {
             uint8_t* wd = w_ring + (s * kKps + h) * L::kW;
             if constexpr (kAct) {
-              // four boxes of 16 gate rows and the 16 up rows of the same columns
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                tma_load_4d<kPair>(wd + b * 32 * kTileK, &tw, fb, (kt + h) * kTileK, wt * 64 + b * 16, 0, t.e, pol_w);
+              // 64 gate rows and the up rows of the same columns
+              tma_load_4d<kPair>(wd, &tw, fb, (kt + h) * kTileK, wt * 64, 0, t.e, pol_w);
             } else {
               tma_load_3d<kPair>(wd, &tw, fb, (kt + h) * kTileK, wt * 128, t.e, pol_w);
             }
-            uint8_t* xd = x_ring + (s * kKps + h) * L::kX;
-            for (int b = 0; b < boxes; ++b)
-              tma_load_rows<kPair>(xd + b * L::kBox * kTileK, &tx, &ctl->full[s], fb, (kt + h) * kTileK,
-                                   xrow + b * L::kBox, pol_x);
+            tma_load_rows<kPair>(x_ring + (s * kKps + h) * L::kX, xmap, &ctl->full[s], fb, (kt + h) * kTileK, xrow,
+                                 pol_x);
           }
           issued = i + 1;
         }
@@ -535,7 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     __syncwarp();
   } else if (busy) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3, et = threadIdx.x - 64;
+    const int q = warp & 3, group = (warp - 2) >> 2, et = (threadIdx.x - 64) & (kEpiThreads - 1);
+    uint8_t* out = groups + group * L::kGroupBytes;
+    float* sx_s = reinterpret_cast<float*>(out + L::kOut);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int lrow = q * 32 + lane;  // row of the weight tile
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
@@ -551,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
       // this thread's weight row and its channel scale (0 past the last row)
       float swv = 0.f;
       if constexpr (kAct) {
-        const int col = t.nt * 64 + q * 16 + (lane & 15);
-        if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * 2 * a.N + (lane >= 16 ? a.N : 0) + col);
+        const int col = t.nt * 64 + (lrow & 63);
+        if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * 2 * a.N + (lrow >= 64 ? a.N : 0) + col);
       } else {
         const int col = t.nt * 128 + lrow;
         if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * a.N + col);
@@ -560,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
       const bool ok = warp_wait(&ctl->tfull[b], (li >> 1) & 1);
       if (!ok && lane == 0) fail(kErrWaitEpilogue);
       if (ok) tc_fence_after();
-      epi_sync();
-      if (et == 0) ctl->epi_ok = !aborted();
-      epi_sync();
-      if (!ctl->epi_ok) break;
+      epi_sync(group);
+      if (et == 0) ctl->epi_ok[group] = !aborted();
+      epi_sync(group);
+      if (!ctl->epi_ok[group]) break;
       const bool whole = !kSplit || (k0 == 0 && k1 == nku);
       int first = me, ncontrib = 1;
       uint32_t* slot = nullptr;
@@ -574,21 +628,23 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         slot = a.partial + (static_cast<size_t>(me) * 2 + (me == first ? 1 : 0)) * (kSwapTileN * kTok) + lrow;
       }
       const int chunks = (t.n + 15) >> 4;
-      for (int c = 0; c < chunks; ++c) {
+      auto release = [&]() {  // this warp has read all it needs of the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(b) * 8u);
+          else mbar_arrive(&ctl->tempty[b]);
+        }
+      };
+      if (group >= chunks) release();
+      for (int c = group; c < chunks; c += kGroups) {
         uint32_t r[16];
         __syncwarp();
         tmem_ld16(taddr + b * kTok + c * 16, r);
         tmem_wait_ld();
-        if (c == chunks - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (kPair) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(b) * 8u);
-            else mbar_arrive(&ctl->tempty[b]);
-          }
-        }
+        if (c + kGroups >= chunks) release();
         if (whole) {
-          finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, flip);
+          finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, group, flip);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) __stcg(slot + (c * 16 + j) * kSwapTileN, r[j]);
@@ -596,13 +652,13 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
       }
       if (!whole) {
         // the last of the tile's CTAs to arrive adds the partials in CTA order
-        epi_sync();
+        epi_sync(group);
         if (et == 0) {
           unsigned old;
           asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.tickets + first) : "memory");
           ctl->last_flag = (old == static_cast<unsigned>(ncontrib - 1));
         }
-        epi_sync();
+        epi_sync(group);
         if (ctl->last_flag) {
           for (int c = 0; c < chunks; ++c) {
             uint32_t sum[16];
@@ -615,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 #pragma unroll
               for (int m = 0; m < 16; ++m) sum[m] = j == 0 ? v[m] : add_acc<kFmt>(sum[m], v[m]);
             }
-            finish16<kFmt, kAct>(a, t, sum, c * 16, swv, sxs, out, flip);
+            finish16<kFmt, kAct>(a, t, sum, c * 16, swv, sxs, out, group, flip);
           }
         }
       }
@@ -671,14 +727,15 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// rows of x in sorted order (offsets), or all of them in place (no offsets)
 template <int kQType>
 cudaError_t launch_quant_t(const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows, const int* order, int div,
-                           uint8_t* q, float* s, cudaStream_t st) {
+                           const int* offsets, int rows, uint8_t* q, float* s, cudaStream_t st) {
   const int vpt = (a.K / 8 + kRowThreads - 1) / kRowThreads;
-  const dim3 grid(a.P), block(kRowThreads);
+  const dim3 grid(rows), block(kRowThreads);
   auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, st, x, a.K, ldx, x_rows, order, div, a.offsets, a.E, a.P, q, s,
-                      a.tickets, a.ctas);
+    return launch_pdl(kernel, grid, block, 0, st, x, a.K, ldx, x_rows, order, div, offsets, a.E, rows, q, s, a.tickets,
+                      a.ctas);
   };
   if (vpt <= 1) return go(experts_quant_kernel<1, kQType>);
   if (vpt <= 2) return go(experts_quant_kernel<2, kQType>);
@@ -687,20 +744,20 @@ cudaError_t launch_quant_t(const ExpertArgs& a, const uint16_t* x, int ldx, int 
   return cudaErrorInvalidValue;
 }
 
-template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, bool kAct>
-cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a, cudaStream_t st) {
-  using L = Layout<kTok, kKps, kPair>;
+template <int kFmt, int kTok, int kKps, bool kSplit, bool kPair, int kGroups, bool kAct>
+cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a, cudaStream_t st) {
+  using L = Layout<kTok, kKps, kPair, kGroups, kAct>;
   static_assert(L::kStages >= 2 && L::kBytes <= kSmemBudget, "ring does not fit");
   // more than half an SM's shared memory, so that no two of these CTAs, which
   // may take all tensor-memory columns, share an SM
   static_assert(L::kBytes > kSmemPerSM / 2, "two CTAs would fit");
-  auto kernel = experts_kernel<kFmt, kTok, kKps, kSplit, kPair, kAct>;
+  auto kernel = experts_kernel<kFmt, kTok, kKps, kSplit, kPair, kGroups, kAct>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, L::kBytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -737,31 +794,45 @@ cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertA
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, tx_short, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int kFmt, bool kAct>
-cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a, cudaStream_t st) {
-  return a.tok <= 64 ? launch_t<kFmt, 64, 2, true, false, kAct>(tw, tx, a, st)
-                     : launch_t<kFmt, 256, 1, false, true, kAct>(tw, tx, a, st);
+cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a, cudaStream_t st) {
+  return a.tok <= 64 ? launch_t<kFmt, 64, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st)
+                     : launch_t<kFmt, 256, 1, false, true, 3, kAct>(tw, tx, tx_short, a, st);
 }
 
 }  // namespace
 
-int experts_box_rows(int tok) { return tok <= 64 ? Layout<64, 2, false>::kBox : Layout<256, 1, true>::kBox; }
-
-cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
-                                 const int* order, int div, uint8_t* q, float* s, cudaStream_t stream) {
-  return fmt == kFmtINT8 ? launch_quant_t<1>(a, x, ldx, x_rows, order, div, q, s, stream)
-                         : launch_quant_t<0>(a, x, ldx, x_rows, order, div, q, s, stream);
+int experts_box_rows(int tok, bool few) {
+  using S = Layout<64, 2, false, 1, false>;
+  using P = Layout<256, 1, true, 3, false>;
+  return tok <= 64 ? (few ? S::kBoxShort : S::kBoxLong) : (few ? P::kBoxShort : P::kBoxLong);
 }
 
-cudaError_t launch_experts(int fmt, bool act, const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a,
+cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
+                                 const int* order, int div, uint8_t* q, float* s, uint8_t* q0, float* s0,
+                                 cudaStream_t stream) {
+  auto quant = [&](const int* ord, const int* offsets, int rows, uint8_t* qd, float* sd) {
+    return fmt == kFmtINT8 ? launch_quant_t<1>(a, x, ldx, x_rows, ord, div, offsets, rows, qd, sd, stream)
+                           : launch_quant_t<0>(a, x, ldx, x_rows, ord, div, offsets, rows, qd, sd, stream);
+  };
+  if (!q0) return quant(order, a.offsets, a.P, q, s);
+  const cudaError_t e = quant(nullptr, nullptr, x_rows, q0, s0);
+  if (e != cudaSuccess) return e;
+  constexpr int kWarps = kPermuteThreads / 32;
+  return launch_pdl(permute_codes_kernel, dim3((a.P + kWarps - 1) / kWarps), dim3(kPermuteThreads), 0, stream,
+                    reinterpret_cast<const uint4*>(q0), static_cast<const float*>(s0), x_rows, order, div, a.offsets,
+                    a.E, a.P, a.K / 16, reinterpret_cast<uint4*>(q), s);
+}
+
+cudaError_t launch_experts(int fmt, bool act, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a,
                            cudaStream_t stream) {
   if (fmt == kFmtINT8)
-    return act ? launch_f<kFmtINT8, true>(tw, tx, a, stream) : launch_f<kFmtINT8, false>(tw, tx, a, stream);
-  return act ? launch_f<kFmtFP8, true>(tw, tx, a, stream) : launch_f<kFmtFP8, false>(tw, tx, a, stream);
+    return act ? launch_f<kFmtINT8, true>(tw, tx, tx_short, a, stream) : launch_f<kFmtINT8, false>(tw, tx, tx_short, a, stream);
+  return act ? launch_f<kFmtFP8, true>(tw, tx, tx_short, a, stream) : launch_f<kFmtFP8, false>(tw, tx, tx_short, a, stream);
 }
 
 cudaError_t read_experts_error(unsigned int* code) {

@@ -175,13 +175,16 @@ struct ExpertArgs {
   int tok;               // most token rows per tile
   int ctas;
 };
-// order: pair at each sorted position (of x row order[i] / div), or null: row i of x
+// order: pair at each sorted position (of x row order[i] / div), or null: row i
+// of x.  q0, s0: null, or codes and scales of the rows of x, each coded once and
+// then copied into sorted order
 cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
-                                 const int* order, int div, uint8_t* q, float* s, cudaStream_t stream);
-// tx: the codes [P][K] in boxes of experts_box_rows(tok) rows
-int experts_box_rows(int tok);
-cudaError_t launch_experts(int fmt, bool act, const CUtensorMap& tw, const CUtensorMap& tx, const ExpertArgs& a,
-                           cudaStream_t stream);
+                                 const int* order, int div, uint8_t* q, float* s, uint8_t* q0, float* s0,
+                                 cudaStream_t stream);
+// tx, tx_short: the codes [P][K] in boxes of experts_box_rows(tok, false / true) rows
+int experts_box_rows(int tok, bool few);
+cudaError_t launch_experts(int fmt, bool act, const CUtensorMap& tw, const CUtensorMap& tx,
+                           const CUtensorMap& tx_short, const ExpertArgs& a, cudaStream_t stream);
 cudaError_t read_experts_error(unsigned int* code);
 cudaError_t clear_experts_error();
 

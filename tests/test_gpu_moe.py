@@ -220,6 +220,33 @@ def test_experts_many_rows(fmt, act, T, k, E, K, N):
 
 
 @pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+def test_experts_rows_taken_often(fmt):
+    # enough rows that each row of x is coded once and its codes are copied; odd widths, dropped pairs
+    _run_experts(fmt, 1400, 8, 16, 1520, 48, True, gather=True, seed=3, dropped=0.05)
+    _run_experts(fmt, 1100, 9, 12, 2064, 144, False, gather=True, seed=5)
+
+
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+@pytest.mark.parametrize("act", [False, True])
+def test_experts_many_tiles_back_to_back(fmt, act):
+    # several tiles per CTA pair and wrapped rings, calls queued behind one another
+    int8 = fmt == "w8a8_int8"
+    T, k, E, K, N = 1500, 4, 4, 1536, 640
+    ids = _ids(T, k, E, 3)
+    off, order, _ = (torch.from_numpy(v) for v in moelib.sort(ids, E))
+    x = torch.randn((T, K), generator=_gen(3)).bfloat16()
+    wq, sw = _weights(E, N * (2 if act else 1), K, int8, 3)
+    args = (qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC, x.cuda(), wq.cuda(), sw.cuda(), off.cuda())
+    kw = dict(order=order.cuda(), top_k=k, act=qgd.ACT_SILU_MUL if act else qgd.ACT_NONE)
+    ys = [qgd.qlinear_experts_bf16(*args, **kw) for _ in range(12)]
+    torch.cuda.synchronize()
+    for y in ys[1:]:
+        assert torch.equal(y.view(torch.int16), ys[0].view(torch.int16))
+    ref, mag = moelib.experts(x, wq, sw, off, order, k, act, int8)
+    moelib.close(ys[0], ref, moelib.experts_tolerance(ref, mag, K, act, int8))
+
+
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
 @pytest.mark.parametrize("counts", [[0, 0, 5, 0], [0, 0, 0, 0], [64, 65, 0, 1], [16, 17, 128, 129], [255, 256, 257, 1],
                                     [600, 0, 3, 0]])
 def test_experts_uneven_loads(fmt, counts):

@@ -104,10 +104,10 @@ def test_workspace_sizes():
     assert qgd.qgd_moe_sort_workspace_size(1, 8) == 0
     assert qgd.qgd_moe_sort_workspace_size(0, 8) == 0
     assert qgd.qgd_moe_sort_workspace_size(1 << 20, 256) >= 256 * 4
-    assert qgd.qgd_experts_workspace_size(qgd.FMT_BLOCK_FP8, 8, 8, 64, 64) == 0
-    assert qgd.qgd_experts_workspace_size(qgd.FMT_W8A8_INT8, 0, 8, 64, 64) == 0
+    assert qgd.qgd_experts_workspace_size(qgd.FMT_BLOCK_FP8, 8, 4, 8, 64, 64) == 0
+    assert qgd.qgd_experts_workspace_size(qgd.FMT_W8A8_INT8, 0, 4, 8, 64, 64) == 0
     # the codes and scales of the sorted rows at least
-    assert qgd.qgd_experts_workspace_size(qgd.FMT_W8A8_INT8, 1000, 8, 64, 512) >= 1000 * 516
+    assert qgd.qgd_experts_workspace_size(qgd.FMT_W8A8_INT8, 1000, 0, 8, 64, 512) >= 1000 * 516
 
 
 # ---------------------------------------------------------------------------
