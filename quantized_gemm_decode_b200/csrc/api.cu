@@ -744,15 +744,17 @@ struct ExpertPlan {
 // x_rows: rows of x behind an order, or 0 without one
 ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
   ExpertPlan p;
-  // few rows per expert: 64-token tiles whose K range is shared out over all
-  // SMs (weights streamed once bound them); many: 256-token tiles
-  p.tok = rows / (rows < E ? rows : E) < 64 ? 64 : 256;
+  // few rows per expert: 64- or 128-token tiles whose K range is shared out
+  // over all SMs (streaming the weights once bounds them); many: 256-token
+  // tiles of CTA pairs
+  const int per_expert = rows / (rows < E ? rows : E);
+  p.tok = per_expert < 40 ? 64 : per_expert < 160 ? 128 : 256;
   p.n_tiles = act ? (N + 63) / 64 : (N + 127) / 128;
   p.ctas = g_num_sms < kMaxExpertCtas ? g_num_sms : kMaxExpertCtas;
   p.q_off = align256(static_cast<size_t>(p.ctas) * 4);
   p.s_off = align256(p.q_off + static_cast<size_t>(rows) * K);
   p.part_off = align256(p.s_off + static_cast<size_t>(rows) * 4);
-  p.total = p.part_off + (p.tok <= 64 ? static_cast<size_t>(p.ctas) * 2 * p.tok * kSwapTileN * 4 : 0);
+  p.total = p.part_off + (p.tok <= 128 ? static_cast<size_t>(p.ctas) * 2 * p.tok * kSwapTileN * 4 : 0);
   // (16 M codes: where the second launch costs less than coding again)
   p.code_once = x_rows > 0 && rows >= 2 * static_cast<long long>(x_rows) && static_cast<long long>(rows) * K >= (1LL << 24);
   if (p.code_once) {

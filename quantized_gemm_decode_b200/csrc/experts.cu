@@ -152,7 +152,8 @@ static_assert(sizeof(Ctl) <= kCtlBytes, "control block too large");
 // x (128 weight rows + kXRows token rows) x 128 bytes; per epilogue group two
 // output staging buffers of 16 tokens x 128 bf16 (with the activation an
 // exchange area of 8 x 128 floats and one buffer of 16 x 64) and the token
-// scales [2][kTok]; control block; running tile counts of the experts.
+// scales [2][kTok]; control block; running tile counts and first rows of the
+// experts.
 template <int kTok, int kKps, bool kPair, int kGroups, bool kAct>
 struct Layout {
   static constexpr int kThreads = 64 + kGroups * kEpiThreads;
@@ -167,7 +168,7 @@ struct Layout {
   static constexpr uint32_t kW = kSwapTileN * kTileK;
   static constexpr uint32_t kX = kXRows * kTileK;
   static constexpr uint32_t kStage = kKps * (kW + kX);
-  static constexpr uint32_t kTail = kGroups * kGroupBytes + kCtlBytes + (kMaxExperts + 1) * 4;
+  static constexpr uint32_t kTail = kGroups * kGroupBytes + kCtlBytes + 2 * (kMaxExperts + 1) * 4;
   static constexpr int kStages0 = static_cast<int>((kSmemBudget - 1024 - kTail) / kStage);
   static constexpr int kStages = kStages0 > kMaxStages ? kMaxStages : kStages0;
   static constexpr size_t kBytes = 1024 + static_cast<size_t>(kStages) * kStage + kTail;
@@ -178,13 +179,17 @@ struct Tile {
   int e, row0, n, nt;
 };
 
-__device__ __forceinline__ int clamp_off(int v, int P) { return v < 0 ? 0 : (v > P ? P : v); }
+// First sorted row of expert e.
+__device__ __forceinline__ int offset_of(const ExpertArgs& a, int e) {
+  const int v = __ldg(a.offsets + e);
+  return v < 0 ? 0 : (v > a.P ? a.P : v);
+}
 
 // Tile w of the list: weight tiles fastest, then an expert's token tiles, then
 // the experts (pre[e]: token tiles of the experts before e).  An expert's rows
 // are dealt to its token tiles evenly, in multiples of kRound.
 template <int kRound>
-__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, int n_tiles, int w) {
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, const int* off, int n_tiles, int w) {
   Tile t;
   const int g = w / n_tiles;
   t.nt = w - g * n_tiles;
@@ -195,8 +200,8 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, i
     else hi = mid;
   }
   t.e = lo;
-  const int o0 = clamp_off(__ldg(a.offsets + lo), a.P), o1 = clamp_off(__ldg(a.offsets + lo + 1), a.P);
-  const int cnt = o1 - o0, tiles = pre[lo + 1] - pre[lo];
+  const int o0 = off[lo];
+  const int cnt = off[lo + 1] - o0, tiles = pre[lo + 1] - pre[lo];
   const int per = ((cnt + tiles - 1) / tiles + kRound - 1) & ~(kRound - 1);
   const int j = g - pre[lo];
   t.row0 = o0 + j * per;
@@ -209,15 +214,16 @@ __device__ __forceinline__ int unit_owner(long long u, long long G, long long U)
 }
 
 // A worker's (CTA's or CTA pair's) work as a sequence of segments (tile, K
-// units [k0, k1)).  kSplit: all (tile, K unit) units dealt out in equal
+// units [k0, k1)).  split: all (tile, K unit) units dealt out in equal
 // contiguous ranges, one per worker, so that every SM streams the same share
 // of the weights; else whole tiles, round-robin.
-template <bool kSplit>
 struct Walk {
-  long long u, ue;  // kSplit: units left; else: next tile and the tile count
-  int nku;
-  __device__ __forceinline__ Walk(int total, int nku_, int worker, int G) : nku(nku_) {
-    if (kSplit) {
+  long long u, ue;  // split: units left; else: next tile and the tile count
+  int nku, G;
+  bool split;
+  __device__ __forceinline__ Walk(int total, int nku_, int worker, int G_, bool split_)
+      : nku(nku_), G(G_), split(split_) {
+    if (split) {
       const long long U = static_cast<long long>(total) * nku;
       u = static_cast<long long>(worker) * U / G;
       ue = static_cast<long long>(worker + 1) * U / G;
@@ -226,9 +232,9 @@ struct Walk {
       ue = total;
     }
   }
-  __device__ __forceinline__ bool next(int& w, int& k0, int& k1, int G) {
+  __device__ __forceinline__ bool next(int& w, int& k0, int& k1) {
     if (u >= ue) return false;
-    if (kSplit) {
+    if (split) {
       w = static_cast<int>(u / nku);
       k0 = static_cast<int>(u - static_cast<long long>(w) * nku);
       const long long left = ue - u;
@@ -395,7 +401,8 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   uint8_t* x_ring = base + stages * kKps * L::kW;
   uint8_t* groups = base + stages * L::kStage;
   Ctl* ctl = reinterpret_cast<Ctl*>(groups + kGroups * L::kGroupBytes);
-  int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + kCtlBytes);
+  int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + kCtlBytes);  // [E + 1]
+  int* off = pre + kMaxExperts + 1;                                               // [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkt = (a.K + kTileK - 1) / kTileK;
@@ -440,7 +447,9 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       const int e = e0 + threadIdx.x;
       int v = 0;
       if (e < a.E) {
-        const int cnt = clamp_off(__ldg(a.offsets + e + 1), a.P) - clamp_off(__ldg(a.offsets + e), a.P);
+        const int first = offset_of(a, e), cnt = offset_of(a, e + 1) - first;
+        off[e] = first;
+        if (e == a.E - 1) off[a.E] = first + cnt;
         v = cnt > 0 ? (cnt + kTok - 1) / kTok : 0;
       }
 #pragma unroll
@@ -467,10 +476,15 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   const int n_tiles = kPair ? (a.n_tiles + 1) / 2 : a.n_tiles;
   const int total = pre[a.E] * n_tiles;
   const long long U = static_cast<long long>(total) * nku;
-  // workers with work: every one gets at least one unit (or tile)
-  const long long most = kSplit ? U : total;
   const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
-  const int G = most < workers ? static_cast<int>(most) : workers;
+  // Whole tiles leave workers idle at the end, split ones cost a hand-over (about
+  // 3 us: partials, arrival, sum); a K unit of 32 KB takes an SM's share of the
+  // bandwidth about 0.75 us: split where idling would be more than kSplitPays units.
+  constexpr int kSplitPays = 4;
+  const int rounds = (total + workers - 1) / workers;
+  const bool split = kSplit && static_cast<long long>(rounds) * nku * workers > U + static_cast<long long>(kSplitPays) * workers;
+  const long long most = split ? U : total;
+  const int G = most < workers ? static_cast<int>(most) : workers;  // workers with work
   const int me = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
   const bool busy = me < G;
   int issued = 0;
@@ -490,17 +504,16 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     if (lane == 0 && busy) {
       const uint64_t pol_w = kSplit ? policy_evict_first() : policy_evict_last();
       const uint64_t pol_x = policy_evict_last();
-      Walk<kSplit> walk(total, nku, me, G);
+      Walk walk(total, nku, me, G, split);
       int w, k0, k1, i = 0;
       bool stop = false;
-      while (!stop && walk.next(w, k0, k1, G)) {
-        const Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+      while (!stop && walk.next(w, k0, k1)) {
+        const Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
         const int wt = kPair ? t.nt * 2 + static_cast<int>(rank) : t.nt;  // this CTA's 128 weight rows
         const int all = (t.n + L::kRound - 1) & ~(L::kRound - 1);
-        const int mine = kPair ? all / 2 : all;            // token rows in this CTA's shared memory
+        const int mine = kPair ? all / 2 : all;  // token rows in this CTA's shared memory
         const int xrow = t.row0 + static_cast<int>(rank) * mine;
-        // rows past the tile's go unused
-        const bool few = mine <= L::kBoxShort;
+        const bool few = mine <= L::kBoxShort;   // rows past the tile's go unused
         const CUtensorMap* xmap = few ? &tx_short : &tx;
         const uint32_t bytes = L::kW + (few ? L::kBoxShort : L::kBoxLong) * kTileK;
         for (int k = k0; k < k1; ++k, ++i) {
@@ -515,19 +528,15 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
             break;
           }
           const int kt = k * kKps, ns = min(kKps, nkt - kt);
+          const uint32_t fb = full0 + static_cast<uint32_t>(s) * 8u;
           // the leader's barrier expects both CTAs' bytes (a copy may land first)
           if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], (kPair ? 2 : 1) * ns * bytes);
-          const uint32_t fb = full0 + static_cast<uint32_t>(s) * 8u;
           for (int h = 0; h < ns; ++h) {
+            const int x = (kt + h) * kTileK;
             uint8_t* wd = w_ring + (s * kKps + h) * L::kW;
-            if constexpr (kAct) {
-              // 64 gate rows and the up rows of the same columns
-              tma_load_4d<kPair>(wd, &tw, fb, (kt + h) * kTileK, wt * 64, 0, t.e, pol_w);
-            } else {
-              tma_load_3d<kPair>(wd, &tw, fb, (kt + h) * kTileK, wt * 128, t.e, pol_w);
-            }
-            tma_load_rows<kPair>(x_ring + (s * kKps + h) * L::kX, xmap, &ctl->full[s], fb, (kt + h) * kTileK, xrow,
-                                 pol_x);
+            if constexpr (kAct) tma_load_4d<kPair>(wd, &tw, fb, x, wt * 64, 0, t.e, pol_w);  // 64 gate rows, their up rows
+            else tma_load_3d<kPair>(wd, &tw, fb, x, wt * 128, t.e, pol_w);
+            tma_load_rows<kPair>(x_ring + (s * kKps + h) * L::kX, xmap, &ctl->full[s], fb, x, xrow, pol_x);
           }
           issued = i + 1;
         }
@@ -538,11 +547,11 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     // ---------------- MMA issuer (of a pair: the leader's) ----------------
     if (lane == 0 && rank == 0 && busy) {
       const uint32_t w_base = smem_u32(w_ring), x_base = smem_u32(x_ring);
-      Walk<kSplit> walk(total, nku, me, G);
+      Walk walk(total, nku, me, G, split);
       int w, k0, k1, i = 0, li = 0;
       bool stop = false;
-      while (!stop && walk.next(w, k0, k1, G)) {
-        const Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+      while (!stop && walk.next(w, k0, k1)) {
+        const Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
         const uint32_t idesc = idesc_mma(kInt ? 2 : 1, kInt ? 1 : 0, (kPair ? 2 : 1) * kSwapTileN,
                                          (t.n + L::kRound - 1) & ~(L::kRound - 1));
         const int b = li & 1;
@@ -593,11 +602,11 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int lrow = q * 32 + lane;  // row of the weight tile
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
-    Walk<kSplit> walk(total, nku, me, G);
+    Walk walk(total, nku, me, G, split);
     int w, k0, k1, li = 0;
     uint32_t flip = 0;
-    while (walk.next(w, k0, k1, G)) {
-      Tile t = find_tile<L::kRound>(a, pre, n_tiles, w);
+    while (walk.next(w, k0, k1)) {
+      Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
       if constexpr (kPair) t.nt = t.nt * 2 + static_cast<int>(rank);
       const int b = li & 1;
       float* sxs = sx_s + b * kTok;
@@ -618,7 +627,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       if (et == 0) ctl->epi_ok[group] = !aborted();
       epi_sync(group);
       if (!ctl->epi_ok[group]) break;
-      const bool whole = !kSplit || (k0 == 0 && k1 == nku);
+      const bool whole = !kSplit || !split || (k0 == 0 && k1 == nku);
       int first = me, ncontrib = 1;
       uint32_t* slot = nullptr;
       if (!whole) {
@@ -799,17 +808,21 @@ cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const CUtenso
 }
 
 template <int kFmt, bool kAct>
-cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a, cudaStream_t st) {
-  return a.tok <= 64 ? launch_t<kFmt, 64, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st)
-                     : launch_t<kFmt, 256, 1, false, true, 3, kAct>(tw, tx, tx_short, a, st);
+cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a,
+                     cudaStream_t st) {
+  switch (a.tok) {
+    case 64: return launch_t<kFmt, 64, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st);
+    case 128: return launch_t<kFmt, 128, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st);
+    case 256: return launch_t<kFmt, 256, 1, false, true, 3, kAct>(tw, tx, tx_short, a, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 int experts_box_rows(int tok, bool few) {
-  using S = Layout<64, 2, false, 1, false>;
-  using P = Layout<256, 1, true, 3, false>;
-  return tok <= 64 ? (few ? S::kBoxShort : S::kBoxLong) : (few ? P::kBoxShort : P::kBoxLong);
+  const int long_rows = tok == 256 ? 128 : tok;  // a pair's CTAs hold half of the tokens each
+  return few ? long_rows / 4 : long_rows;
 }
 
 cudaError_t launch_experts_quant(int fmt, const ExpertArgs& a, const uint16_t* x, int ldx, int x_rows,
