@@ -748,7 +748,7 @@ ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
   // over all SMs (streaming the weights once bounds them); many: 256-token
   // tiles of CTA pairs
   const int per_expert = rows / (rows < E ? rows : E);
-  p.tok = per_expert < 40 ? 64 : per_expert < 160 ? 128 : 256;
+  p.tok = per_expert < 44 ? 64 : per_expert < 112 ? 128 : 256;
   p.n_tiles = act ? (N + 63) / 64 : (N + 127) / 128;
   p.ctas = g_num_sms < kMaxExpertCtas ? g_num_sms : kMaxExpertCtas;
   p.q_off = align256(static_cast<size_t>(p.ctas) * 4);

@@ -56,8 +56,9 @@ __global__ void __launch_bounds__(kRowThreads)
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < ntickets; i += kRowThreads) tickets[i] = 0u;
   const int row = blockIdx.x;
-  const int pair = order ? __ldg(order + row) : row;  // (beside the offset's load, not after it)
-  if (offsets && row >= min(__ldg(offsets + E), P)) return;
+  // the offset is looked at last: its load runs beside those of the order and of x
+  const int live = offsets ? __ldg(offsets + E) : P;
+  const int pair = order ? __ldg(order + row) : row;
   const int src = order ? pair / div : row;
   const bool have = pair >= 0 && src < x_rows;
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(have ? src : 0) * ldx);
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kRowThreads)
       amax = fmaxf(amax, absmax8(v[j]));
     }
   }
+  if (row >= live) return;
   amax = warp_max(amax);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
   __syncthreads();
@@ -209,42 +211,57 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, c
   return t;
 }
 
-__device__ __forceinline__ int unit_owner(long long u, long long G, long long U) {
-  return static_cast<int>(((u + 1) * G - 1) / U);
-}
-
 // A worker's (CTA's or CTA pair's) work as a sequence of segments (tile, K
-// units [k0, k1)).  split: all (tile, K unit) units dealt out in equal
-// contiguous ranges, one per worker, so that every SM streams the same share
-// of the weights; else whole tiles, round-robin.
-struct Walk {
-  long long u, ue;  // split: units left; else: next tile and the tile count
-  int nku, G;
+// units [k0, k1)).  split: all (tile, K unit) units dealt out in contiguous
+// ranges, one per worker, equal up to a unit, so that every SM streams the same
+// share of the weights; else whole tiles, round-robin.  (32-bit arithmetic: a
+// 64-bit division or two here cost each call about half a microsecond.)
+struct Deal {
+  int total, nku, G;
   bool split;
-  __device__ __forceinline__ Walk(int total, int nku_, int worker, int G_, bool split_)
-      : nku(nku_), G(G_), split(split_) {
+  int q, r;  // split: workers before r take q + 1 units, the others q
+  __device__ __forceinline__ Deal(int total_, int nku_, int G_, bool split_)
+      : total(total_), nku(nku_), G(G_), split(split_), q(0), r(0) {
     if (split) {
-      const long long U = static_cast<long long>(total) * nku;
-      u = static_cast<long long>(worker) * U / G;
-      ue = static_cast<long long>(worker + 1) * U / G;
-    } else {
-      u = worker;
-      ue = total;
+      q = total * nku / G;
+      r = total * nku - q * G;
     }
   }
-  __device__ __forceinline__ bool next(int& w, int& k0, int& k1) {
-    if (u >= ue) return false;
+  __device__ __forceinline__ int begin(int worker) const { return worker * q + min(worker, r); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int wide = r * (q + 1);
+    return u < wide ? u / (q + 1) : r + (u - wide) / q;
+  }
+};
+
+struct Walk {
+  int w, k, left, step, nku;  // next segment's tile and first unit; split: units left, else tiles to go
+  bool split;
+  __device__ __forceinline__ Walk(const Deal& d, int worker) : step(d.G), nku(d.nku), split(d.split) {
     if (split) {
-      w = static_cast<int>(u / nku);
-      k0 = static_cast<int>(u - static_cast<long long>(w) * nku);
-      const long long left = ue - u;
-      k1 = left < nku - k0 ? k0 + static_cast<int>(left) : nku;
-      u += k1 - k0;
+      const int u = d.begin(worker);
+      w = u / nku;
+      k = u - w * nku;
+      left = d.q + (worker < d.r ? 1 : 0);
     } else {
-      w = static_cast<int>(u);
-      k0 = 0;
-      k1 = nku;
-      u += G;
+      w = worker;
+      k = 0;
+      left = d.total - worker;
+    }
+  }
+  __device__ __forceinline__ bool next(int& tile, int& k0, int& k1) {
+    if (left <= 0) return false;
+    tile = w;
+    k0 = k;
+    k1 = nku;
+    if (split) {
+      if (left < nku - k) k1 = k + left;
+      left -= k1 - k0;
+      ++w;
+      k = 0;
+    } else {
+      w += step;
+      left -= step;
     }
     return true;
   }
@@ -256,6 +273,12 @@ struct Walk {
 __device__ __forceinline__ void epi_sync(int group) {
   __syncwarp();
   named_bar_sync(1 + group, kEpiThreads);
+}
+
+template <int kGroups>
+__device__ __forceinline__ void all_groups_sync() {
+  __syncwarp();
+  named_bar_sync(1 + 4, kGroups * kEpiThreads);
 }
 
 __device__ __forceinline__ void pair_sync() {
@@ -390,7 +413,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
                    const __grid_constant__ CUtensorMap tx_short, const ExpertArgs a) {
   using L = Layout<kTok, kKps, kPair, kGroups, kAct>;
   constexpr int kThreads = L::kThreads;
-  static_assert(!kSplit || (!kPair && kGroups == 1), "tiles are split between single CTAs with one epilogue group");
+  static_assert(!(kSplit && kPair), "pairs take whole tiles");
   constexpr bool kInt = (kFmt == kFmtINT8);
   constexpr uint32_t kCols = 2 * kTok;  // TMEM: double-buffered accumulator
   constexpr int stages = L::kStages;
@@ -475,16 +498,17 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   const uint32_t tmem = ctl->tmem_base;
   const int n_tiles = kPair ? (a.n_tiles + 1) / 2 : a.n_tiles;
   const int total = pre[a.E] * n_tiles;
-  const long long U = static_cast<long long>(total) * nku;
+  const int U = total * nku;  // (below 2^31: the host checks)
   const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
   // Whole tiles leave workers idle at the end, split ones cost a hand-over (about
   // 3 us: partials, arrival, sum); a K unit of 32 KB takes an SM's share of the
   // bandwidth about 0.75 us: split where idling would be more than kSplitPays units.
   constexpr int kSplitPays = 4;
   const int rounds = (total + workers - 1) / workers;
-  const bool split = kSplit && static_cast<long long>(rounds) * nku * workers > U + static_cast<long long>(kSplitPays) * workers;
-  const long long most = split ? U : total;
-  const int G = most < workers ? static_cast<int>(most) : workers;  // workers with work
+  const bool split = kSplit && (rounds * nku - kSplitPays) * workers > U;
+  const int most = split ? U : total;
+  const int G = most < workers ? most : workers;  // workers with work
+  const Deal deal(total, nku, G > 0 ? G : 1, split);
   const int me = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
   const bool busy = me < G;
   int issued = 0;
@@ -504,7 +528,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     if (lane == 0 && busy) {
       const uint64_t pol_w = kSplit ? policy_evict_first() : policy_evict_last();
       const uint64_t pol_x = policy_evict_last();
-      Walk walk(total, nku, me, G, split);
+      Walk walk(deal, me);
       int w, k0, k1, i = 0;
       bool stop = false;
       while (!stop && walk.next(w, k0, k1)) {
@@ -547,7 +571,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     // ---------------- MMA issuer (of a pair: the leader's) ----------------
     if (lane == 0 && rank == 0 && busy) {
       const uint32_t w_base = smem_u32(w_ring), x_base = smem_u32(x_ring);
-      Walk walk(total, nku, me, G, split);
+      Walk walk(deal, me);
       int w, k0, k1, i = 0, li = 0;
       bool stop = false;
       while (!stop && walk.next(w, k0, k1)) {
@@ -602,7 +626,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int lrow = q * 32 + lane;  // row of the weight tile
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
-    Walk walk(total, nku, me, G, split);
+    Walk walk(deal, me);
     int w, k0, k1, li = 0;
     uint32_t flip = 0;
     while (walk.next(w, k0, k1)) {
@@ -631,9 +655,8 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       int first = me, ncontrib = 1;
       uint32_t* slot = nullptr;
       if (!whole) {
-        const long long u0 = static_cast<long long>(w) * nku;
-        first = unit_owner(u0, G, U);
-        ncontrib = unit_owner(u0 + nku - 1, G, U) - first + 1;
+        first = deal.owner(w * nku);
+        ncontrib = deal.owner(w * nku + nku - 1) - first + 1;
         slot = a.partial + (static_cast<size_t>(me) * 2 + (me == first ? 1 : 0)) * (kSwapTileN * kTok) + lrow;
       }
       const int chunks = (t.n + 15) >> 4;
@@ -661,15 +684,15 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       }
       if (!whole) {
         // the last of the tile's CTAs to arrive adds the partials in CTA order
-        epi_sync(group);
-        if (et == 0) {
+        all_groups_sync<kGroups>();
+        if (threadIdx.x == 64) {
           unsigned old;
           asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.tickets + first) : "memory");
           ctl->last_flag = (old == static_cast<unsigned>(ncontrib - 1));
         }
-        epi_sync(group);
+        all_groups_sync<kGroups>();
         if (ctl->last_flag) {
-          for (int c = 0; c < chunks; ++c) {
+          for (int c = group; c < chunks; c += kGroups) {
             uint32_t sum[16];
             for (int j = 0; j < ncontrib; ++j) {
               const uint32_t* src =
@@ -811,8 +834,8 @@ template <int kFmt, bool kAct>
 cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx_short, const ExpertArgs& a,
                      cudaStream_t st) {
   switch (a.tok) {
-    case 64: return launch_t<kFmt, 64, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st);
-    case 128: return launch_t<kFmt, 128, 2, true, false, 1, kAct>(tw, tx, tx_short, a, st);
+    case 64: return launch_t<kFmt, 64, 2, true, false, 2, kAct>(tw, tx, tx_short, a, st);
+    case 128: return launch_t<kFmt, 128, 2, true, false, 2, kAct>(tw, tx, tx_short, a, st);
     case 256: return launch_t<kFmt, 256, 1, false, true, 3, kAct>(tw, tx, tx_short, a, st);
   }
   return cudaErrorInvalidValue;
