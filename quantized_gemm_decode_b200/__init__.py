@@ -806,13 +806,18 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
     out = (T, top_k if top_k > 0 else 0)
     if weights is None:
         weights = logits.new_empty(out, dtype=torch.float32)
+        wp = weights.data_ptr()
+    else:
+        wp = _operand(weights, "weights", _F32, out, dev)
     if ids is None:
         ids = logits.new_empty(out, dtype=torch.int32)
+        ip = ids.data_ptr()
+    else:
+        ip = _operand(ids, "ids", _I32, out, dev)
     st = (_lib or lib()).moe_route(x, 0 if logits.dtype is torch.bfloat16 else 1, T, E, _row_stride(logits, "logits"),
                                    b, _route_desc(top_k, _SCORES[score], groups, topk_groups, group_top,
                                                   1 if renormalize else 0, scale),
-                                   _operand(weights, "weights", _F32, out, dev), _operand(ids, "ids", _I32, out, dev),
-                                   _raw_stream(dev))
+                                   wp, ip, _raw_stream(dev))
     if st:
         _check(st, "moe_route")
     return weights, ids
@@ -840,17 +845,22 @@ def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=
             return moe_sort(ids, num_experts, offsets, order, pos, ws)
     at = _operand(ids, "ids", _I32, None, dev)
     P = ids.numel()
-    n_off = (num_experts + 1 if num_experts > 0 else 1,)
-    if offsets is None:
-        offsets = ids.new_empty(n_off)
-    if order is None:
-        order = ids.new_empty((P,))
-    if pos is None:
-        pos = ids.new_empty(ids.shape)
+    n_off = num_experts + 1 if num_experts > 0 else 1
+    if offsets is None and order is None and pos is None:
+        # three pieces of one allocation, which costs half of what three do
+        offsets, order, pos = ids.new_empty((n_off + 2 * P,)).split_with_sizes((n_off, P, P))
+        pos = pos.view(ids.shape)
+        fp = offsets.data_ptr()
+        op, pp = fp + 4 * n_off, fp + 4 * (n_off + P)
+    else:
+        offsets = ids.new_empty((n_off,)) if offsets is None else offsets
+        order = ids.new_empty((P,)) if order is None else order
+        pos = ids.new_empty(ids.shape) if pos is None else pos
+        fp = _operand(offsets, "offsets", _I32, (n_off,), dev)
+        op = _operand(order, "order", _I32, (P,), dev)
+        pp = _operand(pos, "pos", _I32, ids.shape, dev)
     wsp, wsn, _keep = _scratch(ws, _sort_need(P, num_experts), ids)
-    st = (_lib or lib()).moe_sort(at, P, num_experts, _operand(offsets, "offsets", _I32, n_off, dev),
-                                  _operand(order, "order", _I32, (P,), dev),
-                                  _operand(pos, "pos", _I32, ids.shape, dev), wsp, wsn, _raw_stream(dev))
+    st = (_lib or lib()).moe_sort(at, P, num_experts, fp, op, pp, wsp, wsn, _raw_stream(dev))
     if st:
         _check(st, "moe_sort")
     return offsets, order, pos
@@ -932,8 +942,11 @@ def moe_combine(h: torch.Tensor, pos, weights, add=None, y=None, stream=None):
         ap, lda = _operand(add, "add", _BF16, (T, H), dev, contiguous=False), _row_stride(add, "add")
     if y is None:
         y = h.new_empty((T, H))
-    st = (_lib or lib()).moe_combine(hp, rows, pp, _operand(weights, "weights", _F32, (T, k), dev), ap, lda,
-                                     _operand(y, "y", _BF16, (T, H), dev), T, k, H, _raw_stream(dev))
+        yp = y.data_ptr()
+    else:
+        yp = _operand(y, "y", _BF16, (T, H), dev)
+    st = (_lib or lib()).moe_combine(hp, rows, pp, _operand(weights, "weights", _F32, (T, k), dev), ap, lda, yp, T, k,
+                                     H, _raw_stream(dev))
     if st:
         _check(st, "moe_combine")
     return y

@@ -15,159 +15,410 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 
 // ---------------------------------------------------------------------------
-// Routing: one warp per token, lane l holding experts l, l + 32, ...
+// Routing: one warp per token, lane l holding kVPT consecutive experts.
 //   x = logit (NaN counts as -inf, +inf as the largest float)
 //   s = exp(x - max) / sum exp(x - max), or 1 / (1 + exp(-x))
 //   choice value c = s + bias; the k largest c of the kept groups, ties to the
 //   lowest index; an expert at -inf is never chosen (id -1, weight 0).
 //   w_j = scale * s_j (/ sum of the chosen s)
-// Values and comparisons are in 64 bits: two experts whose scores are equal in
-// 32 bits would otherwise be ordered by the rounding of an exponential.
-// Without a bias the order of the scores is the order of the logits.
+// The choice is that of 64-bit values: two experts whose scores are equal in 32
+// bits would otherwise be ordered by the rounding of an exponential.  Without a
+// bias the scores' order is the logits', which needs no rounding at all.  With
+// one (and for sums of two scores) a row is first chosen from 32-bit values of
+// known error; only where two values that decide something lie closer than
+// that error, and are not the same logit with the same bias, the row is chosen
+// again in 64 bits (a few rows in a hundred of random ones).  Weights are computed from the chosen logits in 64 bits.
+// 64-bit throughout took 91 us for 16384 rows of 256 experts and 9.3 us for one
+// row; see the table of measurements for this form.
 // ---------------------------------------------------------------------------
-// Order-preserving integer of a double; 0 (below every number's) marks "not a candidate".
-__device__ __forceinline__ unsigned long long sort_key(double v) {
+// Error of a 32-bit score: the fast exponential is within (2 + 1.5 |d|) 2^-23 of
+// exp(-d), times exp(-d) below 2^-21 everywhere; the quotient (softmax: its sum
+// too, at most 32 + 5 additions of positive terms) adds at most 2^-18 of a value
+// below 1.  The sum with the bias rounds once more.
+constexpr float kScoreErr = 0x1p-17f;
+
+template <int kVPT, bool kBf16>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int lane, float (&x)[kVPT]) {
+  const size_t row = static_cast<size_t>(t) * a.ldl;
+  constexpr int kPer = kBf16 ? 8 : 4;  // logits per 16 bytes
+  if constexpr (kVPT >= kPer) {
+    if (a.vec) {  // whole vectors: rows 16-byte aligned, E a multiple of kVPT
+#pragma unroll
+      for (int j = 0; j < kVPT; j += kPer) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        const bool in = lane * kVPT < a.E;
+        if (in)
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.logits) +
+                                                   (row + lane * kVPT + j) * (kBf16 ? 2 : 4)));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float f = kBf16 ? __uint_as_float(i & 1 ? w[i / 2 % 4] & 0xffff0000u : w[i / 2 % 4] << 16)
+                                : __uint_as_float(w[i % 4]);
+          x[j + i] = !in || f != f ? -INFINITY : fminf(f, FLT_MAX);
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) {
+    const int e = lane * kVPT + j;
+    float v = -INFINITY;
+    if (e < a.E) {
+      if constexpr (kBf16)
+        v = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + row + e)) << 16);
+      else
+        v = __ldg(static_cast<const float*>(a.logits) + row + e);
+    }
+    x[j] = v != v ? -INFINITY : fminf(v, FLT_MAX);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int e) {
+  const size_t at = static_cast<size_t>(t) * a.ldl + e;
+  const float v = kBf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + at)) << 16)
+                        : __ldg(static_cast<const float*>(a.logits) + at);
+  return fminf(v, FLT_MAX);
+}
+
+__device__ __forceinline__ float warp_max_f(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// Order-preserving integers (the key 0, below every number's, marks "not a candidate").
+__device__ __forceinline__ unsigned key32(float v) {
+  const unsigned u = __float_as_uint(v + 0.f);
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key32_value(unsigned k) { return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k); }
+__device__ __forceinline__ unsigned warp_max_key(unsigned k) { return __reduce_max_sync(kFull, k); }
+
+__device__ __forceinline__ unsigned long long key64(double v) {
   const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-
-__device__ __forceinline__ double key_value(unsigned long long k) {
+__device__ __forceinline__ double key64_value(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
-
 __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k) {
   const unsigned hi = __reduce_max_sync(kFull, static_cast<unsigned>(k >> 32));
   const unsigned lo = __reduce_max_sync(kFull, static_cast<unsigned>(k >> 32) == hi ? static_cast<unsigned>(k) : 0u);
   return (static_cast<unsigned long long>(hi) << 32) | lo;
 }
 
+struct Key32 {
+  using K = unsigned;
+  using V = float;
+  static __device__ __forceinline__ K key(V v) { return key32(v); }
+  static __device__ __forceinline__ V value(K k) { return key32_value(k); }
+};
+struct Key64 {
+  using K = unsigned long long;
+  using V = double;
+  static __device__ __forceinline__ K key(V v) { return key64(v); }
+  static __device__ __forceinline__ V value(K k) { return key64_value(k); }
+};
+
+// Two largest of two pairs of keys.
+template <typename K>
+__device__ __forceinline__ void merge2(K& b1, K& b2, K o1, K o2) {
+  const K lo = b1 < o1 ? b1 : o1;
+  b1 = b1 < o1 ? o1 : b1;
+  b2 = b2 < o2 ? o2 : b2;
+  b2 = b2 < lo ? lo : b2;
+}
+
+// Clears the keys outside the kept groups.  gkey: the keys that a group's value
+// is made of.  Returns how far the worst kept group's value is above the best
+// other one's (infinity where all or no others are left).
+template <typename T, int kVPT>
+__device__ __forceinline__ typename T::V keep_groups(const RouteArgs& a, int lane, const typename T::K (&gkey)[kVPT],
+                                                     typename T::K (&key)[kVPT]) {
+  using K = typename T::K;
+  using V = typename T::V;
+  const int per = a.E / a.groups;
+  auto group_value = [&](K b1, K b2) -> K { return a.top == 2 && b2 ? T::key(T::value(b1) + T::value(b2)) : b1; };
+  K mine = 0;  // lane g: group g's value
+  const int span = per / kVPT;  // lanes of a group, where groups do not share lanes
+  const bool whole_lanes = per % kVPT == 0 && (span & (span - 1)) == 0;
+  if (whole_lanes) {
+    K b1 = 0, b2 = 0;
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) merge2<K>(b1, b2, gkey[j], K(0));
+    for (int o = 1; o < span; o <<= 1) {
+      const K o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+      merge2<K>(b1, b2, o1, o2);
+    }
+    const K v = group_value(b1, b2);
+    mine = __shfl_sync(kFull, v, lane * span & 31);
+    if (lane >= a.groups) mine = 0;
+  } else {
+    for (int g = 0; g < a.groups; ++g) {
+      K b1 = 0, b2 = 0;
+#pragma unroll
+      for (int j = 0; j < kVPT; ++j) {
+        const int e = lane * kVPT + j;
+        merge2<K>(b1, b2, e >= g * per && e < (g + 1) * per ? gkey[j] : K(0), K(0));
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const K o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+        merge2<K>(b1, b2, o1, o2);
+      }
+      const K v = group_value(b1, b2);
+      if (lane == g) mine = v;
+    }
+  }
+  // a group's rank: the groups before it in the order of values, then of indices
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const K v = __shfl_sync(kFull, mine, g);
+    rank += v > mine || (v == mine && g < lane) ? 1 : 0;
+  }
+  const bool in = lane < a.groups && rank < a.keep;
+  const unsigned kept = __ballot_sync(kFull, in);
+  if (whole_lanes) {
+    const bool mine_kept = (kept >> (lane / span & 31)) & 1u;
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) key[j] = mine_kept ? key[j] : K(0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) {
+      const int e = lane * kVPT + j;
+      if (e < a.E && !((kept >> (e / per)) & 1u)) key[j] = 0;
+    }
+  }
+  const K last = ~warp_max_key(in ? ~mine : K(0)), next = warp_max_key(in ? K(0) : mine);
+  return last && next ? T::value(last) - T::value(next) : static_cast<V>(INFINITY);
+}
+
+__device__ __forceinline__ double exact_score(bool sigmoid, float x, float mx) {
+  if (!(x > -INFINITY)) return 0.0;
+  return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : exp(static_cast<double>(x) - static_cast<double>(mx));
+}
+
+// Weights of the chosen experts (lane i: the i-th, its logit xs) and the row's
+// outputs.  total: the softmax's sum, where the weights are not renormalised.
+__device__ __forceinline__ void write_row(const RouteArgs& a, int t, int lane, int id, float xs, float mx, double total) {
+  double w = id >= 0 ? exact_score(a.sigmoid, xs, mx) : 0.0;
+  if (a.renorm) {
+    double sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (sum > 0.0) w /= sum;
+  } else if (!a.sigmoid && total > 0.0) {
+    w /= total;
+  }
+  if (lane < a.k) {
+    a.weights[static_cast<size_t>(t) * a.k + lane] = static_cast<float>(w * static_cast<double>(a.scale));
+    a.ids[static_cast<size_t>(t) * a.k + lane] = id;
+  }
+}
+
+// A row in 64 bits.
+template <int kVPT, bool kBf16>
+__device__ __noinline__ void route_row_exact(const RouteArgs& a, int t, int lane) {
+  using K = Key64::K;
+  float x[kVPT];
+  load_logits<kVPT, kBf16>(a, t, lane, x);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) mx = fmaxf(mx, x[j]);
+  mx = warp_max_f(mx);
+  double s[kVPT], total = 0.0;
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) {
+    s[j] = exact_score(a.sigmoid, x[j], mx);
+    total += s[j];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+  K key[kVPT], gkey[kVPT];
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) {
+    const int e = lane * kVPT + j;
+    const double v = a.sigmoid ? s[j] : (total > 0.0 ? s[j] / total : 0.0);
+    const double c = a.bias ? v + static_cast<double>(e < a.E ? __ldg(a.bias + e) : 0.f) : static_cast<double>(x[j]);
+    const bool can = x[j] > -INFINITY && c > -INFINITY;  // (a bias of -inf or NaN excludes too)
+    key[j] = can ? key64(c) : 0;
+    gkey[j] = a.top == 2 && !a.bias && can ? key64(v) : key[j];
+  }
+  if (a.keep < a.groups) keep_groups<Key64, kVPT>(a, lane, gkey, key);
+  int my_id = -1;
+  float my_x = 0.f;
+  for (int i = 0; i < a.k; ++i) {
+    K b = 0;
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) b = key[j] > b ? key[j] : b;
+    const K best = warp_max_key(b);
+    if (best == 0) break;
+    const int owner = __ffs(__ballot_sync(kFull, b == best)) - 1;
+    int at = -1;
+    float xv = 0.f;
+#pragma unroll
+    for (int j = kVPT - 1; j >= 0; --j)
+      if (key[j] == best) {
+        at = j;
+        xv = x[j];
+      }
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j)
+      if (lane == owner && j == at) key[j] = 0;
+    at = __shfl_sync(kFull, at, owner);
+    xv = __shfl_sync(kFull, xv, owner);
+    if (lane == i) {
+      my_id = owner * kVPT + at;
+      my_x = xv;
+    }
+  }
+  write_row(a, t, lane, my_id, my_x, mx, total);
+}
+
 constexpr int kRouteWarps = 4;
 
 template <int kVPT, bool kBf16>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  const int E = a.E;
-  float x[kVPT];
+  float x[kVPT], bias[kVPT];
+  load_logits<kVPT, kBf16>(a, t, lane, x);
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) bias[j] = 0.f;
+  if (a.bias) {
+    if (kVPT >= 4 && a.vec_bias) {
+#pragma unroll
+      for (int j = 0; j + 3 < kVPT; j += 4)
+        if (lane * kVPT < a.E) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + lane * kVPT + j));
+          bias[j] = f.x;
+          bias[j + 1] = f.y;
+          bias[j + 2] = f.z;
+          bias[j + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVPT; ++j)
+        if (lane * kVPT + j < a.E) bias[j] = __ldg(a.bias + lane * kVPT + j);
+    }
+  }
   float mx = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kVPT; ++j) {
-    const int e = j * 32 + lane;
-    x[j] = -INFINITY;
-    if (e < E) {
-      const size_t at = static_cast<size_t>(t) * a.ldl + e;
-      if constexpr (kBf16)
-        x[j] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + at)) << 16);
-      else
-        x[j] = __ldg(static_cast<const float*>(a.logits) + at);
-      x[j] = x[j] != x[j] ? -INFINITY : fminf(x[j], FLT_MAX);
-    }
-    mx = fmaxf(mx, x[j]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-  // scores
-  double s[kVPT];
-  if (a.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j) s[j] = x[j] > -INFINITY ? 1.0 / (1.0 + exp(-static_cast<double>(x[j]))) : 0.0;
-  } else {
-    double sum = 0.0;
-#pragma unroll
+  for (int j = 0; j < kVPT; ++j) mx = fmaxf(mx, x[j]);
+  mx = warp_max_f(mx);
+  const bool grouped = a.keep < a.groups;
+  const bool by_score = a.bias != nullptr || (grouped && a.top == 2);  // scores decide something
+  const bool need_total = !a.sigmoid && !a.renorm;
+  double total = 0.0;
+  if (need_total) {
+    // the weights' denominator: exponentials within 2^-22, the rounding of x - max undone to first order
     for (int j = 0; j < kVPT; ++j) {
-      s[j] = x[j] > -INFINITY ? exp(static_cast<double>(x[j]) - static_cast<double>(mx)) : 0.0;
-      sum += s[j];
+      if (x[j] > -INFINITY) {
+        const double d = static_cast<double>(x[j]) - static_cast<double>(mx);
+        const float r = static_cast<float>(d);
+        total += static_cast<double>(expf(r)) * (1.0 + (d - static_cast<double>(r)));
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j) s[j] *= inv;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
   }
-  // choice keys; with groups, gkey holds what a group's value is made of
-  unsigned long long key[kVPT];
+  // keys of the choice: the value's upper bits, then the index inside the lane
+  // (lowest first among equals), so that a key names its expert
+  constexpr unsigned kIdx = kVPT - 1;  // kVPT is a power of two
+  constexpr float kCut = kVPT * 0x1p-23f;  // what the index's bits cut off a value, relative
+  unsigned key[kVPT];
+  bool sure = true;
+  float s[kVPT];
+  if (by_score) {
+    if (a.sigmoid) {
 #pragma unroll
-  for (int j = 0; j < kVPT; ++j) {
-    const int e = j * 32 + lane;
-    const double c = a.bias ? s[j] + static_cast<double>(e < E ? __ldg(a.bias + e) : 0.f) : static_cast<double>(x[j]);
-    key[j] = x[j] > -INFINITY && c > -INFINITY ? sort_key(c) : 0ull;  // (a bias of -inf or NaN excludes too)
-  }
-  if (a.keep < a.groups) {
-    const int per = E / a.groups;
-    unsigned long long mine = 0ull;  // lane g: group g's value
-    for (int g = 0; g < a.groups; ++g) {
-      // the lane's two best of the group, then the warp's
-      unsigned long long b1 = 0ull, b2 = 0ull;
+      for (int j = 0; j < kVPT; ++j) s[j] = __fdividef(1.f, 1.f + __expf(fminf(-x[j], 80.f)));
+    } else {
+      float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kVPT; ++j) {
-        const int e = j * 32 + lane;
-        unsigned long long v = e >= g * per && e < (g + 1) * per ? key[j] : 0ull;
-        if (a.top == 2 && !a.bias && v) v = sort_key(s[j]);
-        if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
+        s[j] = x[j] > -INFINITY ? __expf(x[j] - mx) : 0.f;
+        sum += s[j];
       }
-      const unsigned long long m1 = warp_max_key(b1);
-      unsigned long long value = m1;
-      if (a.top == 2 && m1) {
-        const unsigned owner = __ffs(__ballot_sync(kFull, b1 == m1)) - 1;
-        const unsigned long long m2 = warp_max_key(lane == static_cast<int>(owner) ? b2 : b1);
-        if (m2) value = sort_key(key_value(m1) + key_value(m2));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kVPT; ++j) s[j] *= inv;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) {
+    const float c = a.bias ? s[j] + bias[j] : x[j];
+    key[j] = x[j] > -INFINITY && c > -INFINITY ? key32(c) : 0u;
+  }
+  if (grouped) {
+    const bool sums = a.top == 2 && !a.bias;
+    unsigned gkey[kVPT];
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) gkey[j] = sums && key[j] ? key32(s[j]) : key[j];
+    const float gap = keep_groups<Key32, kVPT>(a, lane, gkey, key);
+    if (by_score) {
+      // (a group's value: up to two choice values, each off by the score's error and a rounding of the sum)
+      float most = 0.f;
+#pragma unroll
+      for (int j = 0; j < kVPT; ++j) most = fmaxf(most, fabsf(bias[j]));
+      most = warp_max_f(most);
+      sure = gap > 4.f * kScoreErr + (1.f + most) * 0x1p-20f;
+    }
+  }
+  unsigned b = 0u;
+#pragma unroll
+  for (int j = 0; j < kVPT; ++j) {
+    key[j] = key[j] ? (key[j] & ~kIdx) | (kIdx - j) : 0u;
+    b = key[j] > b ? key[j] : b;
+  }
+  // The k best; lane i keeps the i-th.  Neighbours in the order must be further
+  // apart than their errors (without a bias: than the cut) or equal by
+  // construction (same logit, same bias), up to the first value that is clearly
+  // below the last one chosen.
+  int my_id = -1, prev = -1;
+  unsigned prev_key = 0u;
+  bool clear = false;
+  for (int i = 0; sure && (i < a.k || !clear); ++i) {
+    const unsigned most = warp_max_key(b);
+    if (most == 0u) break;
+    const int owner = __ffs(__ballot_sync(kFull, (b | kIdx) == (most | kIdx))) - 1;  // the lowest lane of equals
+    const unsigned best = __shfl_sync(kFull, b, owner);
+    const int id = owner * kVPT + static_cast<int>(kIdx - (best & kIdx));
+    if (i > 0) {
+      bool apart = (prev_key ^ best) > kIdx;  // the cut keys differ: so do the logits
+      if (a.bias) {
+        const float hi = key32_value(prev_key & ~kIdx), lo = key32_value(best | kIdx);
+        apart = hi - lo > 2.f * kScoreErr + (fabsf(hi) + fabsf(lo)) * (kCut + 0x1p-22f);
       }
-      if (lane == g) mine = value;
+      if (!apart)
+        sure = logit_at<kBf16>(a, t, id) == logit_at<kBf16>(a, t, prev) &&
+               (!a.bias || __ldg(a.bias + id) == __ldg(a.bias + prev));
+      clear = i >= a.k && apart;
     }
-    unsigned kept = 0u;
-    for (int i = 0; i < a.keep; ++i) {
-      const unsigned long long best = warp_max_key(mine);
-      if (best == 0ull) break;
-      const int g = __ffs(__ballot_sync(kFull, mine == best)) - 1;
-      kept |= 1u << g;
-      if (lane == g) mine = 0ull;
-    }
+    prev = id;
+    prev_key = best;
+    if (lane == i && i < a.k) my_id = id;
+    const unsigned gone = lane == owner ? best : 0xffffffffu;
+    b = 0u;
 #pragma unroll
     for (int j = 0; j < kVPT; ++j) {
-      const int e = j * 32 + lane;
-      if (e < E && !((kept >> (e / per)) & 1u)) key[j] = 0ull;
+      key[j] = key[j] == gone ? 0u : key[j];
+      b = key[j] > b ? key[j] : b;
     }
   }
-  // the k best; lane i keeps the i-th
-  double my_s = 0.0;
-  int my_id = -1;
-  for (int i = 0; i < a.k; ++i) {
-    unsigned long long b = 0ull;
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j) b = key[j] > b ? key[j] : b;
-    const unsigned long long best = warp_max_key(b);
-    if (best == 0ull) break;
-    unsigned at = 0xffffffffu;
-#pragma unroll
-    for (int j = kVPT - 1; j >= 0; --j)
-      if (key[j] == best) at = j * 32 + lane;
-    at = __reduce_min_sync(kFull, at);
-    double sv = 0.0;
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j)
-      if (static_cast<unsigned>(j * 32 + lane) == at) {
-        sv = s[j];
-        key[j] = 0ull;
-      }
-    sv = __shfl_sync(kFull, sv, at & 31);
-    if (lane == i) {
-      my_s = sv;
-      my_id = static_cast<int>(at);
-    }
+  if (!sure) {
+    route_row_exact<kVPT, kBf16>(a, t, lane);
+    return;
   }
-  if (a.renorm) {
-    double sum = my_s;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (sum > 0.0) my_s /= sum;
-  }
-  if (lane < a.k) {
-    a.weights[static_cast<size_t>(t) * a.k + lane] = static_cast<float>(my_s * static_cast<double>(a.scale));
-    a.ids[static_cast<size_t>(t) * a.k + lane] = my_id;
-  }
+  write_row(a, t, lane, my_id, my_id >= 0 ? logit_at<kBf16>(a, t, my_id) : 0.f, mx, total);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,16 +620,24 @@ cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned block,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int kVPT, bool kBf16>
+cudaError_t launch_route_v(RouteArgs a, cudaStream_t st) {
+  const bool whole = a.E % kVPT == 0;
+  a.vec = whole && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && static_cast<size_t>(a.ldl) * (kBf16 ? 2 : 4) % 16 == 0;
+  a.vec_bias = whole && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+  return launch_pdl(route_kernel<kVPT, kBf16>, static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps),
+                    kRouteWarps * 32, 0, st, a);
+}
+
 template <bool kBf16>
 cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps), block = kRouteWarps * 32;
   const int vpt = (a.E + 31) / 32;
-  if (vpt <= 1) return launch_pdl(route_kernel<1, kBf16>, grid, block, 0, st, a);
-  if (vpt <= 2) return launch_pdl(route_kernel<2, kBf16>, grid, block, 0, st, a);
-  if (vpt <= 4) return launch_pdl(route_kernel<4, kBf16>, grid, block, 0, st, a);
-  if (vpt <= 8) return launch_pdl(route_kernel<8, kBf16>, grid, block, 0, st, a);
-  if (vpt <= 16) return launch_pdl(route_kernel<16, kBf16>, grid, block, 0, st, a);
-  return launch_pdl(route_kernel<32, kBf16>, grid, block, 0, st, a);
+  if (vpt <= 1) return launch_route_v<1, kBf16>(a, st);
+  if (vpt <= 2) return launch_route_v<2, kBf16>(a, st);
+  if (vpt <= 4) return launch_route_v<4, kBf16>(a, st);
+  if (vpt <= 8) return launch_route_v<8, kBf16>(a, st);
+  if (vpt <= 16) return launch_route_v<16, kBf16>(a, st);
+  return launch_route_v<32, kBf16>(a, st);
 }
 
 }  // namespace
