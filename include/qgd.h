@@ -374,7 +374,7 @@ QGD_API qgd_status moe_route(const void* logits, int logits_dtype, int T, int E,
  * positions offsets[e] .. offsets[e+1] - 1; order [pairs]: the pair at each
  * sorted position, -1 behind the last; pos [pairs]: the sorted position of
  * each pair, -1 where it was dropped.  pairs == 0 writes offsets only (all
- * zero).  Workspace: qgd_moe_sort_workspace_size() bytes, 4-byte aligned
+ * zero).  Workspace: qgd_moe_sort_workspace_size() bytes, 16-byte aligned
  * (NULL when 0). */
 QGD_API size_t qgd_moe_sort_workspace_size(int pairs, int E);
 QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws,

@@ -697,6 +697,7 @@ def qgd_w8a8_int8_acc32(xq, wq, acc=None, ws=None, stream=None):
 # Mixture of experts
 # ---------------------------------------------------------------------------
 _I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_LOGITS, _INT8, _E4M3 = (torch.float32, torch.bfloat16), (torch.int8,), (torch.float8_e4m3fn, torch.uint8)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -726,18 +727,21 @@ def _device_of(t, name: str) -> int:
 
 def _operand(t, name: str, dtypes, shape, device: int, contiguous: bool = True) -> int:
     """Check an operand (shape None: any); returns its address.  These calls are a
-    few microseconds long on the GPU, so the checks are kept to attribute reads."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
+    few microseconds long on the GPU, so a good operand passes on attribute reads
+    alone, and what is wrong with a bad one is found out afterwards."""
+    try:
+        if t.dtype in dtypes and t.get_device() == device and (shape is None or t.shape == shape) \
+                and (not contiguous or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -801,7 +805,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     T, E = logits.shape
-    x = _operand(logits, "logits", (torch.float32, torch.bfloat16), None, dev, contiguous=False)
+    x = _operand(logits, "logits", _LOGITS, None, dev, False)
     b = None if bias is None else _operand(bias, "bias", _F32, (E,), dev)
     out = (T, top_k if top_k > 0 else 0)
     if weights is None:
@@ -898,7 +902,7 @@ def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None,
         raise ValueError("x must be 2-D")
     xp = _operand(x, "x", _BF16, None, dev, contiguous=False)
     x_rows, K = x.shape
-    wp = _operand(wq, "wq", (torch.int8,) if fmt == FMT_W8A8_INT8 else (torch.float8_e4m3fn, torch.uint8), None, dev)
+    wp = _operand(wq, "wq", _INT8 if fmt == FMT_W8A8_INT8 else _E4M3, None, dev)
     if wq.dim() != 3 or wq.shape[2] != K:
         raise ValueError(f"wq must be [experts, rows, K={K}], got {tuple(wq.shape)}")
     E, n_all, _ = wq.shape

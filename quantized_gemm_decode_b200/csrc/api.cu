@@ -1098,8 +1098,7 @@ qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl
 
 size_t qgd_moe_sort_workspace_size(int pairs, int E) {
   if (pairs <= 0 || E <= 0 || E > kMaxExperts) return 0;
-  const int blocks = sort_blocks(pairs, E);
-  return blocks > 1 ? align256(static_cast<size_t>(blocks) * E * 4) : 0;
+  return align256(sort_workspace(pairs, E));
 }
 
 qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws, size_t ws_bytes,
@@ -1107,8 +1106,8 @@ qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, 
   if (pairs < 0 || E <= 0) return fail(QGD_ERR_INVALID, "bad sizes (pairs=%d E=%d)", pairs, E);
   if (E > kMaxExperts) return fail(QGD_ERR_UNSUPPORTED, "E=%d experts (at most %d)", E, kMaxExperts);
   if (!offsets || (pairs > 0 && (!ids || !order || !pos))) return fail(QGD_ERR_INVALID, "null pointer");
-  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(pos) || !aligned4(ws))
-    return fail(QGD_ERR_INVALID, "pointers must be 4-byte aligned");
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(pos) || !aligned16(ws))
+    return fail(QGD_ERR_INVALID, "pointers must be 4-byte aligned, the workspace 16-byte");
   const size_t need = qgd_moe_sort_workspace_size(pairs, E);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(QGD_ERR_WORKSPACE, "sort workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : 0);

@@ -31,11 +31,12 @@ constexpr uint32_t kFull = 0xffffffffu;
 // 64-bit throughout took 91 us for 16384 rows of 256 experts and 9.3 us for one
 // row; see the table of measurements for this form.
 // ---------------------------------------------------------------------------
-// Error of a 32-bit score: the fast exponential is within (2 + 1.5 |d|) 2^-23 of
-// exp(-d), times exp(-d) below 2^-21 everywhere; the quotient (softmax: its sum
-// too, at most 32 + 5 additions of positive terms) adds at most 2^-18 of a value
-// below 1.  The sum with the bias rounds once more.
-constexpr float kScoreErr = 0x1p-17f;
+// Error of a 32-bit score.  The fast exponential is within (2 + 1.2 |d|) 2^-23 of
+// exp(-d), relative.  Sigmoid, 1 / (1 + e): at most 0.63 * 2^-23 from e, then the
+// sum's and the quotient's roundings, below 2^-21.5 together.  Softmax: the sum of
+// up to 1024 positive terms (32 in a lane, 5 exchanges) is off by 37 * 2^-24 and by
+// its terms' weighted error, at most 8 * 2^-23: with the quotient below 2^-18.
+constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-18f;
 
 template <int kVPT, bool kBf16>
 __device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int lane, float (&x)[kVPT]) {
@@ -201,17 +202,53 @@ __device__ __forceinline__ double exact_score(bool sigmoid, float x, float mx) {
   return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : exp(static_cast<double>(x) - static_cast<double>(mx));
 }
 
+// exp(x) within 1e-11: x = n ln 2 + r, |r| <= ln 2 / 2, the series of exp(r) to its
+// ninth power, times 2^n.  (The library's function, for its last bits, takes about
+// five times the instructions.)
+__device__ __forceinline__ double exp_series(double x) {
+  if (!(fabs(x) < 700.0)) return exp(x);
+  const double n = rint(x * 1.4426950408889634);
+  const double r = fma(-n, 0.6931471805599453, x);
+  double p = 1.0 / 362880.0;
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return p * __hiloint2double((static_cast<int>(n) + 1023) << 20, 0);
+}
+
+// 1 / d to about 2^-46 for d in fp32's range: a 32-bit reciprocal and one Newton step.
+__device__ __forceinline__ double reciprocal(double d) {
+  const double r = static_cast<double>(__frcp_rn(static_cast<float>(d)));
+  return fma(r, fma(-d, r, 1.0), r);
+}
+
 // Weights of the chosen experts (lane i: the i-th, its logit xs) and the row's
 // outputs.  total: the softmax's sum, where the weights are not renormalised.
 __device__ __forceinline__ void write_row(const RouteArgs& a, int t, int lane, int id, float xs, float mx, double total) {
-  double w = id >= 0 ? exact_score(a.sigmoid, xs, mx) : 0.0;
+  double w = 0.0;
+  if (id >= 0) {
+    if (a.sigmoid) {
+      const double e = exp_series(-static_cast<double>(xs));
+      w = e < 1e30 ? reciprocal(1.0 + e) : 1.0 / (1.0 + e);
+    } else {
+      w = exp_series(static_cast<double>(xs) - static_cast<double>(mx));
+    }
+  }
+  double sum = total;
   if (a.renorm) {
-    double sum = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (sum > 0.0) w /= sum;
-  } else if (!a.sigmoid && total > 0.0) {
-    w /= total;
+    sum = w;
+    for (int o = 1; o < a.k; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    sum = __shfl_sync(kFull, sum, 0);
+  }
+  if (a.renorm || !a.sigmoid) {
+    if (sum > 1e-30 && sum < 1e30) w *= reciprocal(sum);
+    else if (sum > 0.0) w /= sum;
   }
   if (lane < a.k) {
     a.weights[static_cast<size_t>(t) * a.k + lane] = static_cast<float>(w * static_cast<double>(a.scale));
@@ -334,6 +371,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   constexpr float kCut = kVPT * 0x1p-23f;  // what the index's bits cut off a value, relative
   unsigned key[kVPT];
   bool sure = true;
+  const float err = a.sigmoid ? kSigmoidErr : kSoftmaxErr;
   float s[kVPT];
   if (by_score) {
     if (a.sigmoid) {
@@ -370,7 +408,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
 #pragma unroll
       for (int j = 0; j < kVPT; ++j) most = fmaxf(most, fabsf(bias[j]));
       most = warp_max_f(most);
-      sure = gap > 4.f * kScoreErr + (1.f + most) * 0x1p-20f;
+      sure = gap > 4.f * err + (1.f + most) * 0x1p-20f;
     }
   }
   unsigned b = 0u;
@@ -379,33 +417,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     key[j] = key[j] ? (key[j] & ~kIdx) | (kIdx - j) : 0u;
     b = key[j] > b ? key[j] : b;
   }
-  // The k best; lane i keeps the i-th.  Neighbours in the order must be further
-  // apart than their errors (without a bias: than the cut) or equal by
-  // construction (same logit, same bias), up to the first value that is clearly
-  // below the last one chosen.
-  int my_id = -1, prev = -1;
-  unsigned prev_key = 0u;
-  bool clear = false;
-  for (int i = 0; sure && (i < a.k || !clear); ++i) {
+  // The k best and one more; lane i keeps the i-th.
+  int my_id = -1;
+  unsigned my_key = 0u, last_key = 0u;  // last: the one behind the k
+  const int rounds = sure ? a.k + 1 : 0;
+  for (int i = 0; i < rounds; ++i) {
     const unsigned most = warp_max_key(b);
     if (most == 0u) break;
     const int owner = __ffs(__ballot_sync(kFull, (b | kIdx) == (most | kIdx))) - 1;  // the lowest lane of equals
     const unsigned best = __shfl_sync(kFull, b, owner);
     const int id = owner * kVPT + static_cast<int>(kIdx - (best & kIdx));
-    if (i > 0) {
-      bool apart = (prev_key ^ best) > kIdx;  // the cut keys differ: so do the logits
-      if (a.bias) {
-        const float hi = key32_value(prev_key & ~kIdx), lo = key32_value(best | kIdx);
-        apart = hi - lo > 2.f * kScoreErr + (fabsf(hi) + fabsf(lo)) * (kCut + 0x1p-22f);
-      }
-      if (!apart)
-        sure = logit_at<kBf16>(a, t, id) == logit_at<kBf16>(a, t, prev) &&
-               (!a.bias || __ldg(a.bias + id) == __ldg(a.bias + prev));
-      clear = i >= a.k && apart;
+    if (i == a.k) {
+      last_key = best;
+    } else if (lane == i) {
+      my_id = id;
+      my_key = best;
     }
-    prev = id;
-    prev_key = best;
-    if (lane == i && i < a.k) my_id = id;
     const unsigned gone = lane == owner ? best : 0xffffffffu;
     b = 0u;
 #pragma unroll
@@ -414,83 +441,123 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       b = key[j] > b ? key[j] : b;
     }
   }
+  // Neighbours in the order must be further apart than their errors (without a
+  // bias: than the cut) or equal by construction (same logit, same bias); the
+  // first one left out must be apart, since its equals behind it were not seen.
+  const float my_x = my_id >= 0 ? logit_at<kBf16>(a, t, my_id) : 0.f;
+  const float my_b = a.bias && my_id >= 0 ? __ldg(a.bias + my_id) : 0.f;
+  if (a.bias || !kBf16) {  // (the cut takes nothing from a bf16 logit: its keys are exact)
+    const unsigned down = __shfl_down_sync(kFull, my_key, 1);
+    const float next_x = __shfl_down_sync(kFull, my_x, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
+    const unsigned next = lane == a.k - 1 ? last_key : down;
+    bool ok = true;
+    if (lane < a.k && my_key && next) {
+      ok = (my_key ^ next) > kIdx;  // the cut keys differ: so do the logits
+      if (a.bias) {
+        const float hi = key32_value(my_key & ~kIdx), lo = key32_value(next | kIdx);
+        ok = hi - lo > 2.f * err + (fabsf(hi) + fabsf(lo)) * (kCut + 0x1p-22f);
+      }
+      ok = ok || (lane < a.k - 1 && my_x == next_x && my_b == next_b);
+    }
+    sure = sure && __all_sync(kFull, ok);
+  }
   if (!sure) {
     route_row_exact<kVPT, kBf16>(a, t, lane);
     return;
   }
-  write_row(a, t, lane, my_id, my_id >= 0 ? logit_at<kBf16>(a, t, my_id) : 0.f, mx, total);
+  write_row(a, t, lane, my_id, my_x, mx, total);
 }
 
 // ---------------------------------------------------------------------------
-// Sort of the pairs by expert (stable counting sort).  A block takes
-// kSortRounds x 32 consecutive pairs per warp; each warp counts its own pairs
-// per expert in shared memory, the counts become start positions (experts
-// before, blocks before, warps before), and a second pass over the same pairs
-// places them, 32 at a time: a pair's rank among the 32 is the number of
-// lower lanes with the same expert.
+// Sort of the pairs by expert (stable counting sort).  A warp takes kRounds x 32
+// consecutive pairs and counts them per expert in shared memory; the counts
+// become start positions (experts before, blocks before, warps before), and a
+// second pass over the same pairs places them, 32 at a time: a pair's rank among
+// the 32 is the number of lower lanes with the same expert.  One block does a
+// decode step; more blocks first count their pairs in a kernel of their own.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 8;
-constexpr int kSortChunk = kSortThreads * kSortRounds;  // pairs per block
+constexpr int kSortRounds = 4;                          // several blocks: rounds per warp
+constexpr int kSortChunk = kSortThreads * kSortRounds;  // and pairs per block
 
-// Counts of this block's pairs per expert.
+__host__ __device__ inline int count_stride(int E) { return (E + 3) & ~3; }  // a block's row of counts, whole vectors
+
+// Counts of each block's pairs per expert.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __restrict__ ids, int P, int E,
                                                                   int* __restrict__ counts) {
   extern __shared__ int hist[];
   griddep_launch_dependents();
-  griddep_wait();
   for (int e = threadIdx.x; e < E; e += kSortThreads) hist[e] = 0;
   __syncthreads();
+  griddep_wait();
   const long long p0 = static_cast<long long>(blockIdx.x) * kSortChunk;
+  int id[kSortRounds];
 #pragma unroll
   for (int r = 0; r < kSortRounds; ++r) {
     const long long p = p0 + r * kSortThreads + threadIdx.x;
-    const int e = p < P ? __ldg(ids + p) : -1;
-    if (e >= 0 && e < E) atomicAdd(hist + e, 1);
+    id[r] = p < P ? __ldg(ids + p) : -1;
   }
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r)
+    if (id[r] >= 0 && id[r] < E) atomicAdd(hist + id[r], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) counts[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
+  const int stride = count_stride(E);
+  for (int e = threadIdx.x; e < stride; e += kSortThreads)
+    counts[static_cast<size_t>(blockIdx.x) * stride + e] = e < E ? hist[e] : 0;
 }
 
+template <int kRounds>
 __global__ void __launch_bounds__(kSortThreads)
     sort_place_kernel(const int* __restrict__ ids, int P, int E, int* __restrict__ offsets, int* __restrict__ order,
                       int* __restrict__ pos, const int* __restrict__ counts) {
   extern __shared__ int sh[];
-  int* cnt = sh;                       // [warps][E]: a warp's count, then its next position
-  int* total = sh + kSortWarps * E;    // [E]: pairs of the expert in all blocks, then its first position
-  int* before = total + E;             // [E]: pairs of the expert in the blocks before
+  const int stride = count_stride(E);
+  int* cnt = sh;                            // [warps][E]: a warp's count, then its next position
+  int* total = sh + kSortWarps * stride;    // [E]: pairs of the expert in all blocks, then its first position
+  int* before = total + stride;             // [E]: pairs of the expert in the blocks before
   __shared__ int scan[kSortWarps + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool alone = gridDim.x == 1;
   griddep_launch_dependents();
-  griddep_wait();
-  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < (kSortWarps + 2) * stride; i += kSortThreads) sh[i] = 0;
   __syncthreads();
-  const long long p0 = static_cast<long long>(blockIdx.x) * kSortChunk + warp * (32 * kSortRounds) + lane;
-  int id[kSortRounds];
+  griddep_wait();
+  const long long p0 = static_cast<long long>(blockIdx.x) * (kSortThreads * kRounds) + warp * (32 * kRounds) + lane;
+  int id[kRounds];
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
     const long long p = p0 + r * 32;
     const int e = p < P ? __ldg(ids + p) : -1;
     id[r] = e >= 0 && e < E ? e : -1;
-    if (id[r] >= 0) atomicAdd(cnt + warp * E + id[r], 1);
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) {
-    int all = 0, prior = 0;
-    if (gridDim.x == 1) {
-      for (int w = 0; w < kSortWarps; ++w) all += cnt[w * E + e];
-    } else {
+  if (!alone) {
+    // the blocks' counts, four experts a thread, the blocks dealt to as many threads as there are
+    const int vecs = stride / 4, teams = kSortThreads / vecs;
+    const int team = threadIdx.x / vecs, v = threadIdx.x - team * vecs;
+    if (team < teams) {
+      int4 all = make_int4(0, 0, 0, 0), prior = all;
 #pragma unroll 8
-      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-        const int c = __ldg(counts + static_cast<size_t>(b) * E + e);
-        all += c;
-        prior += b < static_cast<int>(blockIdx.x) ? c : 0;
+      for (int b = team; b < static_cast<int>(gridDim.x); b += teams) {
+        const int4 c = __ldg(reinterpret_cast<const int4*>(counts + static_cast<size_t>(b) * stride) + v);
+        const int m = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+        all = make_int4(all.x + c.x, all.y + c.y, all.z + c.z, all.w + c.w);
+        prior = make_int4(prior.x + (c.x & m), prior.y + (c.y & m), prior.z + (c.z & m), prior.w + (c.w & m));
+      }
+      const int s4[4] = {all.x, all.y, all.z, all.w}, p4[4] = {prior.x, prior.y, prior.z, prior.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (s4[i]) atomicAdd(total + 4 * v + i, s4[i]);
+        if (p4[i]) atomicAdd(before + 4 * v + i, p4[i]);
       }
     }
-    total[e] = all;
-    before[e] = prior;
   }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (id[r] >= 0) {
+      atomicAdd(cnt + warp * stride + id[r], 1);
+      if (alone) atomicAdd(total + id[r], 1);
+    }
   __syncthreads();
   // exclusive sum over the experts
   int carry = 0;
@@ -506,36 +573,40 @@ __global__ void __launch_bounds__(kSortThreads)
     if (lane == 31) scan[warp] = v;
     __syncthreads();
     int lead = carry, all = carry;
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      if (w < warp) lead += scan[w];
-      all += scan[w];
+      const int c = scan[w];
+      lead += w < warp ? c : 0;
+      all += c;
     }
-    if (e < E) total[e] = lead + v - own;
+    if (e < E) {
+      const int first = lead + v - own;
+      if (blockIdx.x == 0) offsets[e] = first;
+      // the warps' start positions of this expert
+      int c[kSortWarps], at = first + before[e];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = cnt[w * stride + e];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        cnt[w * stride + e] = at;
+        at += c[w];
+      }
+    }
     carry = all;
     __syncthreads();
   }
-  if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e < E; e += kSortThreads) offsets[e] = total[e];
-    if (threadIdx.x == 0) offsets[E] = carry;
-  }
-  for (int e = threadIdx.x; e < E; e += kSortThreads) {
-    int at = total[e] + before[e];
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = cnt[w * E + e];
-      cnt[w * E + e] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = carry;
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
     const long long p = p0 + r * 32;
     const unsigned same = __match_any_sync(kFull, id[r]);
     int at = -1;
-    if (id[r] >= 0) at = cnt[warp * E + id[r]] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (id[r] >= 0 && lane == __ffs(same) - 1) cnt[warp * E + id[r]] += __popc(same);
-    __syncwarp();
+    if (id[r] >= 0) at = cnt[warp * stride + id[r]] + __popc(same & ((1u << lane) - 1u));
+    if constexpr (kRounds > 1) {
+      __syncwarp();
+      if (id[r] >= 0 && lane == __ffs(same) - 1) cnt[warp * stride + id[r]] += __popc(same);
+      __syncwarp();
+    }
     if (p < P) {
       pos[p] = at;
       if (at >= 0) order[at] = static_cast<int>(p);
@@ -646,25 +717,35 @@ cudaError_t launch_route(const RouteArgs& a, bool bf16, cudaStream_t stream) {
   return bf16 ? launch_route_t<true>(a, stream) : launch_route_t<false>(a, stream);
 }
 
-int sort_blocks(int P, int E) {
-  (void)E;
-  return static_cast<int>((static_cast<long long>(P) + kSortChunk - 1) / kSortChunk);
+int sort_blocks(int P) { return static_cast<int>((static_cast<long long>(P) + kSortChunk - 1) / kSortChunk); }
+
+size_t sort_workspace(int P, int E) {
+  const int blocks = sort_blocks(P);
+  return blocks > 1 ? static_cast<size_t>(blocks) * count_stride(E) * 4 : 0;
+}
+
+template <int kRounds>
+static cudaError_t launch_place(unsigned blocks, const int* ids, int P, int E, int* offsets, int* order, int* pos,
+                                const int* counts, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e =
+      allow_smem(sort_place_kernel<kRounds>, static_cast<size_t>(kSortWarps + 2) * kMaxExperts * 4, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(sort_place_kernel<kRounds>, blocks, kSortThreads,
+                    static_cast<size_t>(kSortWarps + 2) * count_stride(E) * 4, stream, ids, P, E, offsets, order, pos,
+                    counts);
 }
 
 cudaError_t launch_sort(const int* ids, int P, int E, int* offsets, int* order, int* pos, int* counts,
                         cudaStream_t stream) {
-  const unsigned blocks = P > 0 ? static_cast<unsigned>(sort_blocks(P, E)) : 1u;
-  cudaError_t e;
+  if (P <= kSortThreads) return launch_place<1>(1, ids, P, E, offsets, order, pos, counts, stream);
+  const unsigned blocks = static_cast<unsigned>(sort_blocks(P));
   if (blocks > 1) {
-    e = launch_pdl(sort_count_kernel, blocks, kSortThreads, static_cast<size_t>(E) * 4, stream, ids, P, E, counts);
+    const cudaError_t e =
+        launch_pdl(sort_count_kernel, blocks, kSortThreads, static_cast<size_t>(E) * 4, stream, ids, P, E, counts);
     if (e != cudaSuccess) return e;
   }
-  const size_t smem = static_cast<size_t>(kSortWarps + 2) * E * 4;
-  static std::atomic<uint64_t> done{0};
-  e = allow_smem(sort_place_kernel, static_cast<size_t>(kSortWarps + 2) * kMaxExperts * 4, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(sort_place_kernel, blocks, kSortThreads, smem, stream, ids, P, E, offsets, order, pos,
-                    static_cast<const int*>(counts));
+  return launch_place<kSortRounds>(blocks, ids, P, E, offsets, order, pos, counts, stream);
 }
 
 cudaError_t launch_combine(const uint16_t* h, int P, const int* pos, const float* weights, const uint16_t* add, int lda,

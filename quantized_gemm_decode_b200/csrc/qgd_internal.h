@@ -156,8 +156,8 @@ struct RouteArgs {
 };
 cudaError_t launch_route(const RouteArgs& a, bool bf16, cudaStream_t stream);
 
-// counts: [blocks][E] scratch of sort_blocks(P, E) blocks (none for one block)
-int sort_blocks(int P, int E);
+// counts: sort_workspace(P, E) bytes of scratch, 16-byte aligned (none where it is 0)
+size_t sort_workspace(int P, int E);
 cudaError_t launch_sort(const int* ids, int P, int E, int* offsets, int* order, int* pos, int* counts,
                         cudaStream_t stream);
 cudaError_t launch_combine(const uint16_t* h, int P, const int* pos, const float* weights, const uint16_t* add, int lda,
