@@ -719,6 +719,11 @@ def _on(device: int, stream) -> contextlib.ExitStack:
     return stack
 
 
+def _new(dtype, *shape) -> torch.Tensor:
+    """An output on the current device (the spelling that costs the least)."""
+    return torch.empty(*shape, dtype=dtype, device="cuda")
+
+
 def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -764,7 +769,7 @@ def _scratch(ws, need: int, like: torch.Tensor) -> tuple:
     if need == 0:
         return None, 0, None
     if ws is None:
-        ws = like.new_empty((need,), dtype=torch.uint8)
+        ws = _new(torch.uint8, need)
     else:
         if isinstance(ws, Workspace):
             ws = ws.ensure(need).buf
@@ -809,12 +814,12 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
     b = None if bias is None else _operand(bias, "bias", _F32, (E,), dev)
     out = (T, top_k if top_k > 0 else 0)
     if weights is None:
-        weights = logits.new_empty(out, dtype=torch.float32)
+        weights = _new(torch.float32, *out)
         wp = weights.data_ptr()
     else:
         wp = _operand(weights, "weights", _F32, out, dev)
     if ids is None:
-        ids = logits.new_empty(out, dtype=torch.int32)
+        ids = _new(torch.int32, *out)
         ip = ids.data_ptr()
     else:
         ip = _operand(ids, "ids", _I32, out, dev)
@@ -850,18 +855,20 @@ def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=
     at = _operand(ids, "ids", _I32, None, dev)
     P = ids.numel()
     n_off = num_experts + 1 if num_experts > 0 else 1
-    if offsets is None and order is None and pos is None:
-        # three pieces of one allocation, which costs half of what three do
-        offsets, order, pos = ids.new_empty((n_off + 2 * P,)).split_with_sizes((n_off, P, P))
-        pos = pos.view(ids.shape)
+    if offsets is None:
+        offsets = _new(torch.int32, n_off)
         fp = offsets.data_ptr()
-        op, pp = fp + 4 * n_off, fp + 4 * (n_off + P)
     else:
-        offsets = ids.new_empty((n_off,)) if offsets is None else offsets
-        order = ids.new_empty((P,)) if order is None else order
-        pos = ids.new_empty(ids.shape) if pos is None else pos
         fp = _operand(offsets, "offsets", _I32, (n_off,), dev)
+    if order is None:
+        order = _new(torch.int32, P)
+        op = order.data_ptr()
+    else:
         op = _operand(order, "order", _I32, (P,), dev)
+    if pos is None:
+        pos = torch.empty_like(ids)
+        pp = pos.data_ptr()
+    else:
         pp = _operand(pos, "pos", _I32, ids.shape, dev)
     wsp, wsn, _keep = _scratch(ws, _sort_need(P, num_experts), ids)
     st = (_lib or lib()).moe_sort(at, P, num_experts, fp, op, pp, wsp, wsn, _raw_stream(dev))
@@ -914,12 +921,14 @@ def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None,
         op = _operand(order, "order", _I32, None, dev)
         rows = order.numel()
     if y is None:
-        y = x.new_empty((rows, N))
+        y = _new(torch.bfloat16, rows, N)
+        yp = y.data_ptr()
+    else:
+        yp = _operand(y, "y", _BF16, (rows, N), dev)
     wsp, wsn, _keep = _scratch(ws, _experts_need(dev, fmt, rows, 0 if op is None else x_rows, E, N, K, act), x)
     st = (_lib or lib()).qlinear_experts_bf16(fmt, xp, _row_stride(x, "x"), x_rows, op, top_k,
                                               _operand(offsets, "offsets", _I32, (E + 1,), dev), E, rows, wp,
-                                              _operand(sw, "sw", _F32, (E, n_all), dev),
-                                              _operand(y, "y", _BF16, (rows, N), dev), N, K, act, wsp, wsn,
+                                              _operand(sw, "sw", _F32, (E, n_all), dev), yp, N, K, act, wsp, wsn,
                                               _raw_stream(dev))
     if st:
         _check(st, "qlinear_experts_bf16")
@@ -945,7 +954,7 @@ def moe_combine(h: torch.Tensor, pos, weights, add=None, y=None, stream=None):
     if add is not None:
         ap, lda = _operand(add, "add", _BF16, (T, H), dev, contiguous=False), _row_stride(add, "add")
     if y is None:
-        y = h.new_empty((T, H))
+        y = _new(torch.bfloat16, T, H)
         yp = y.data_ptr()
     else:
         yp = _operand(y, "y", _BF16, (T, H), dev)

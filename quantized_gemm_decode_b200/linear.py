@@ -109,6 +109,99 @@ class QuantizedLinear:
         return y
 
 
+class QuantizedExperts:
+    """The feed-forward layer of a mixture of experts on quantized weights: for
+    each token t with router logits l[t],
+
+        y[t] = add[t] + sum over its top_k experts e of
+               w[t, e] * down_e(silu(gate_e(x[t])) * up_e(x[t]))
+
+    with the choice and weights w of moe_route, weights quantized once at
+    construction (per output channel) and activations dynamically by every
+    call (FP8_Dynamic or W8A8_INT8).  Six kernel steps, none of which reads
+    device data on the host: the choice, the pairs' sort, the two grouped
+    products with their quantizers, and the weighted sum.
+
+    w_gate_up [E, 2I, H] (gate rows before up rows) and w_down [E, H, I] are
+    bf16; or pass `weights` = (gate_up codes, scales, down codes, scales) as
+    the grouped products take them.  `route` holds moe_route's options
+    (score, bias, groups, topk_groups, group_top, renormalize, scale).
+
+    A call up to GRAPH_MAX_M tokens replays the graph of its bucket once
+    capture() has run (rows behind the call's tokens are padding, routed to no
+    expert); other calls launch directly.  Direct calls may overlap (other
+    streams); a captured bucket's buffers are shared by its replays, which
+    must not."""
+
+    def __init__(self, w_gate_up, w_down, top_k: int, fmt: str = "w8a8_int8", route: dict | None = None,
+                 weights: tuple | None = None):
+        if fmt not in ("fp8_dynamic", "w8a8_int8"):
+            raise ValueError(f"experts take fp8_dynamic or w8a8_int8, not {fmt}")
+        self.fmt, self.fmt_id, self.top_k = fmt, _FMT[fmt], int(top_k)
+        self.route = dict(route or {})
+        if weights is None:
+            weights = self._quantize(w_gate_up) + self._quantize(w_down)
+        self.gate_up, self.gate_up_s, self.down, self.down_s = weights
+        self.E, two_i, self.H = self.gate_up.shape
+        self.I = two_i // 2
+        if two_i % 2 or tuple(self.down.shape) != (self.E, self.H, self.I):
+            raise ValueError(f"gate_up {tuple(self.gate_up.shape)} and down {tuple(self.down.shape)} do not match")
+        self.device = self.gate_up.device
+        self._graphs: dict = {}
+
+    def _quantize(self, w: torch.Tensor) -> tuple:
+        E, rows, K = w.shape
+        qt = qgd.QTYPE_INT8 if self.fmt == "w8a8_int8" else qgd.QTYPE_E4M3
+        wq, sw = qgd.quant_weight_per_channel(w.reshape(E * rows, K), qt)
+        return wq.view(E, rows, K), sw.view(E, rows)
+
+    def layer(self, x: torch.Tensor, logits: torch.Tensor, add=None, y=None) -> torch.Tensor:
+        """The layer on x [T, H] bf16 and logits [T, E] (bf16 or fp32), on the
+        current stream; either may be a column slice of a wider matrix."""
+        if x.shape[0] != logits.shape[0] or logits.shape[1] != self.E or x.shape[1] != self.H:
+            raise ValueError(f"x {tuple(x.shape)} and logits {tuple(logits.shape)} for {self.E} experts of width {self.H}")
+        w, ids = qgd.moe_route(logits, self.top_k, **self.route)
+        offsets, order, pos = qgd.moe_sort(ids, self.E)
+        h = qgd.qlinear_experts_bf16(self.fmt_id, x, self.gate_up, self.gate_up_s, offsets, order=order,
+                                     top_k=self.top_k, act=qgd.ACT_SILU_MUL)
+        o = qgd.qlinear_experts_bf16(self.fmt_id, h, self.down, self.down_s, offsets)
+        return qgd.moe_combine(o, pos, w, add=add, y=y)
+
+    def capture(self, buckets=DECODE_BUCKETS, logits_dtype=torch.float32) -> None:
+        """Capture one graph per M bucket (static buffers for x, logits, add and y)."""
+        for mb in buckets:
+            x = torch.zeros((mb, self.H), dtype=torch.bfloat16, device=self.device)
+            add = torch.zeros_like(x)
+            logits = torch.full((mb, self.E), float("-inf"), dtype=logits_dtype, device=self.device)
+            y = torch.empty_like(x)
+            s = torch.cuda.Stream(self.device)
+            s.wait_stream(torch.cuda.current_stream(self.device))
+            with torch.cuda.stream(s):
+                self.layer(x, logits, add=add, y=y)  # warm-up outside capture
+            torch.cuda.current_stream(self.device).wait_stream(s)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.device(self.device), torch.cuda.graph(g):
+                self.layer(x, logits, add=add, y=y)
+            self._graphs[mb] = (g, x, logits, add, y)
+
+    def __call__(self, x: torch.Tensor, logits: torch.Tensor, add=None) -> torch.Tensor:
+        M = x.shape[0]
+        mb = qgd.qgd_m_bucket(M) if 0 < M <= GRAPH_MAX_M else 0
+        if mb not in self._graphs:
+            return self.layer(x, logits, add=add)
+        g, xs, ls, adds, ys = self._graphs[mb]
+        xs[:M].copy_(x, non_blocking=True)
+        ls[:M].copy_(logits, non_blocking=True)
+        if M < mb:
+            ls[M:].fill_(float("-inf"))
+        if add is None:
+            adds.zero_()
+        else:
+            adds[:M].copy_(add, non_blocking=True)
+        g.replay()
+        return ys[:M]
+
+
 class DecodeStep:
     """One decode step of several quantized linear layers captured as a single
     CUDA graph, host I/O included: each layer's activations are copied from

@@ -360,3 +360,156 @@ def test_a_layer_of_experts(fmt, T):
     oc[n:] = 0
     ref, mag = moelib.combine(oc, pos.cpu(), w.cpu(), x)
     moelib.close(y, ref, moelib.combine_tolerance(ref, mag, k))
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, devices, the layer class
+# ---------------------------------------------------------------------------
+def _layer(fmt="w8a8_int8", E=8, H=256, I=96, k=3, **route):
+    from quantized_gemm_decode_b200.linear import QuantizedExperts
+    g = _gen(E + H)
+    gu = (0.05 * torch.randn((E, 2 * I, H), generator=g)).bfloat16().cuda()
+    dn = (0.05 * torch.randn((E, H, I), generator=g)).bfloat16().cuda()
+    return QuantizedExperts(gu, dn, k, fmt, route=route), gu, dn
+
+
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+def test_layer_class_graphs_match_direct_calls(fmt):
+    layer, _, _ = _layer(fmt, score="sigmoid", groups=4, topk_groups=2, group_top=2)
+    layer.capture(buckets=(1, 4, 8))
+    g = _gen(1)
+    for M in (1, 2, 4, 3, 7, 8, 9, 40, 1):
+        x = torch.randn((M, 256), generator=g).bfloat16().cuda()
+        lg = torch.randn((M, 8), generator=g).cuda()
+        add = torch.randn((M, 256), generator=g).bfloat16().cuda() if M % 2 else None
+        y = layer(x, lg, add=add).clone()
+        ref = layer.layer(x, lg, add=add)
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), ref.view(torch.int16)), M
+
+
+def test_layer_class_against_its_formula():
+    layer, gu, dn = _layer()
+    T, k, E = 21, 3, 8
+    g = _gen(2)
+    x = torch.randn((T, 256), generator=g).bfloat16()
+    lg = torch.randn((T, E), generator=g)
+    y = layer.layer(x.cuda(), lg.cuda()).double().cpu()
+    w, ids = moelib.route(lg, k)
+    ref = torch.zeros((T, 256), dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            v = gu[e].double().cpu() @ x[t].double()
+            h = v[:96] / (1 + torch.exp(-v[:96])) * v[96:]
+            ref[t] += w[t, j] * (dn[e].double().cpu() @ h)
+    # the whole layer in 8 bits against none: a sanity check on the error's norm
+    assert (y - ref).norm() / ref.norm() < 0.05
+
+
+def test_layer_class_refuses_what_does_not_fit():
+    layer, gu, dn = _layer()
+    from quantized_gemm_decode_b200.linear import QuantizedExperts
+    with pytest.raises(ValueError):
+        QuantizedExperts(gu, dn[:, :, :64], 2)
+    with pytest.raises(ValueError):
+        QuantizedExperts(gu, dn, 2, "block_fp8")
+    with pytest.raises(ValueError):
+        layer.layer(torch.zeros((2, 256), device="cuda").bfloat16(), torch.zeros((3, 8), device="cuda"))
+    with pytest.raises(qgd.QGDError):
+        qgd.moe_route(torch.zeros((2, 8), device="cuda"), 9)
+    assert layer(torch.zeros((0, 256), device="cuda").bfloat16(), torch.zeros((0, 8), device="cuda")).shape == (0, 256)
+
+
+def test_two_graphs_and_two_streams_at_once():
+    # each call brings its own workspace: graphs captured separately may run side by side
+    layer, _, _ = _layer(E=16, H=512, I=208, k=4)
+    ins, refs, graphs, outs = [], [], [], []
+    for i in range(2):
+        g = _gen(50 + i)
+        x = torch.randn((24 + 200 * i, 512), generator=g).bfloat16().cuda()
+        lg = torch.randn((24 + 200 * i, 16), generator=g).cuda()
+        refs.append(layer.layer(x, lg).clone())
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            y = layer.layer(x, lg)
+        ins.append((x, lg))
+        graphs.append(gr)
+        outs.append(y)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for y, r in zip(outs, refs):
+        assert torch.equal(y.view(torch.int16), r.view(torch.int16))
+    # and direct calls on two streams, given as an argument
+    got = [None, None]
+    for rep in range(10):
+        for i, s in enumerate(streams):
+            x, lg = ins[i]
+            w, ids = qgd.moe_route(lg, 4, stream=s)
+            off, order, pos = qgd.moe_sort(ids, 16, stream=s)
+            h = qgd.qlinear_experts_bf16(layer.fmt_id, x, layer.gate_up, layer.gate_up_s, off, order=order, top_k=4,
+                                         act=qgd.ACT_SILU_MUL, stream=s)
+            o = qgd.qlinear_experts_bf16(layer.fmt_id, h, layer.down, layer.down_s, off, stream=s.cuda_stream)
+            got[i] = qgd.moe_combine(o, pos, w, stream=s)
+    torch.cuda.synchronize()
+    for y, r in zip(got, refs):
+        assert torch.equal(y.view(torch.int16), r.view(torch.int16))
+
+
+def test_replay_follows_new_routings():
+    layer, _, _ = _layer(E=8, H=256, I=96, k=2)
+    x = torch.randn((40, 256), generator=_gen(4)).bfloat16().cuda()
+    lg = torch.randn((40, 8), generator=_gen(5)).cuda()
+    layer.layer(x, lg)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        y = layer.layer(x, lg)
+    for seed in range(3):
+        new = torch.randn((40, 8), generator=_gen(60 + seed))
+        if seed == 1:
+            new[:, 1:] = float("-inf")  # everything to one expert, one slot each
+        if seed == 2:
+            new[:] = float("-inf")      # nothing to anyone
+        lg.copy_(new)
+        gr.replay()
+        torch.cuda.synchronize()
+        ref = layer.layer(x, new.cuda())
+        assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+        if seed == 2:
+            assert not y.any()
+
+
+def test_caller_workspace_and_buffers():
+    E, K, N, T, k = 6, 256, 96, 33, 2
+    wq, sw = _weights(E, N, K, True, 1)
+    ids = _ids(T, k, E, 8)
+    x = torch.randn((T, K), generator=_gen(8)).bfloat16().cuda()
+    off, order, pos = qgd.moe_sort(ids.cuda(), E)
+    need = qgd.qgd_experts_workspace_size(qgd.FMT_W8A8_INT8, T * k, T, E, N, K)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # no zero-filling needed
+    a = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, x, wq.cuda(), sw.cuda(), off, order=order, top_k=k, ws=ws)
+    b = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, x, wq.cuda(), sw.cuda(), off, order=order, top_k=k,
+                                 ws=qgd.Workspace(16))
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    with pytest.raises(qgd.QGDError):
+        qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, x, wq.cuda(), sw.cuda(), off, order=order, top_k=k, ws=ws[:64])
+
+
+def test_a_row_listed_twice():
+    # an order that names rows of x itself (top_k 1), the same one several times
+    E, K, N = 3, 128, 32
+    wq, sw = _weights(E, N, K, False, 1)
+    x = torch.randn((4, K), generator=_gen(1)).bfloat16()
+    order = torch.tensor([2, 2, 0, 3, 2, 2, 1], dtype=torch.int32)
+    off = torch.tensor([0, 3, 3, 7], dtype=torch.int32)
+    y = qgd.qlinear_experts_bf16(qgd.FMT_FP8_DYNAMIC, x.cuda(), wq.cuda(), sw.cuda(), off.cuda(), order=order.cuda())
+    ref, mag = moelib.experts(x, wq, sw, off, order, 1, False, False)
+    moelib.close(y, ref, moelib.experts_tolerance(ref, mag, K, False, False))
+    assert torch.equal(y[0].view(torch.int16), y[1].view(torch.int16))
