@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kRowThreads)
   amax = fmaxf(amax, kAmaxFloor);
   const float sc = __fdiv_rn(amax, kQType == 0 ? kE4M3Max : kInt8Max);
   if (threadIdx.x == 0) s[row] = sc;
-  const float inv = 1.f / sc;
+  const Reciprocals inv = reciprocals(sc);
 #pragma unroll
   for (int j = 0; j < kVPT; ++j) {
     const int idx = threadIdx.x + j * kRowThreads;
@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // Many rows that several experts take: each row of x is coded once and the
-// codes are copied into sorted order, a warp per row.  Coding costs about 20
-// issue slots a value, so coding k times is bound by the SMs (181 us for 65536
-// rows of 4096, 8 per row of x) where the copy is bound by its stores.
+// codes are copied into sorted order, a warp per row: coding costs about 10
+// issue slots a value, so coding k times is bound by the SMs where the copy is
+// bound by its stores.
 constexpr int kPermuteThreads = 256;
 
 __global__ void __launch_bounds__(kPermuteThreads)

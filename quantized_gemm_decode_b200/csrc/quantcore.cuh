@@ -61,45 +61,53 @@ __device__ __forceinline__ uint2 encode8(const uint4& v, float s) {
   return out;
 }
 
-// The same 8 codes as encode8 with a division only where it could matter:
-// t = x * inv, inv = 1 / s rounded, is within 1.5 * 2^-23 (relative) of the
-// rounded quotient x / s, so both round to one code unless a rounding boundary
-// lies within that distance of t; only then (or for a NaN) the quotient is
-// computed.  s is between 2^-49 and 2^122 (or infinite, inv = 0), so inv is normal.
-//   e4m3, |t| in [2^-6, 512): boundaries where the 20 low bits of the fp32
-//     mantissa are 0x80000; 8 steps of distance are allowed for.  Below 2^-11
-//     every value rounds to zero.  In between (e4m3's subnormals) it divides.
-//   int8: boundaries at k + 1/2, |t| < 128: an absolute distance of 2^-15
-//     covers it.  Adding 1.5 * 2^23 rounds half to even in the sum's low bits.
-// A correctly rounded division costs about 35 issue slots a value on B200,
-// this about 6: 75 -> 35 us for 65536 rows of 1024.
+// The same 8 codes as encode8 with a division only where it could matter.
+// Reciprocals a little below and a little above 1 / s (kSpread, eight fp32 steps;
+// their own rounding, the product's and the quotient's are below two) enclose the
+// rounded quotient x / s.  Rounding to a code is monotone, so where both ends give
+// one code that is the quotient's; only else (and for a NaN in int8) it divides.
+//   e4m3: both ends converted, two values at a time; a NaN converts to NaN either way.
+//   int8: adding 1.5 * 2^23 in the fused product rounds to an integer, half to
+//     even, in the sum's low bits; a NaN is unequal to itself and divides.
+// s is between 2^-49 and 2^122 (or infinite, both reciprocals 0).  A correctly
+// rounded division costs about 35 issue slots a value on B200.
+constexpr float kSpread = 0x1p-20f;
+
+struct Reciprocals {
+  float lo, hi;
+};
+__device__ __forceinline__ Reciprocals reciprocals(float s) {
+  const float inv = 1.f / s;
+  return {inv * (1.f - kSpread), inv * (1.f + kSpread)};
+}
+
 template <int kQType>
-__device__ __forceinline__ uint2 encode8_by_reciprocal(const uint4& v, float s, float inv) {
+__device__ __forceinline__ uint2 encode8_by_reciprocal(const uint4& v, float s, const Reciprocals& inv) {
   const float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
                       bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
   uint2 out;
   if constexpr (kQType == 0) {
-    float d[8];
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d[i] = f[i] * inv;
-      const uint32_t bits = __float_as_uint(d[i]) & 0x7fffffffu;
-      const bool clear = ((bits + 8u) & 0xfffffu) - 0x80000u > 16u && bits - 0x3c800000u < 0x07800000u;
-      if (!clear && !(bits < 0x3a000000u)) d[i] = __fdiv_rn(f[i], s);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = e4m3x2(f[2 * i] * inv.lo, f[2 * i + 1] * inv.lo);
+      c[i] = e4m3x2(f[2 * i] * inv.hi, f[2 * i + 1] * inv.hi);
+      if (lo != c[i]) c[i] = e4m3x2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s));
     }
-    out.x = e4m3x2(d[0], d[1]) | (e4m3x2(d[2], d[3]) << 16);
-    out.y = e4m3x2(d[4], d[5]) | (e4m3x2(d[6], d[7]) << 16);
+    out.x = c[0] | (c[1] << 16);
+    out.y = c[2] | (c[3] << 16);
   } else {
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = f[i] * inv;
-      const float r = t + 12582912.f;
-      c[i] = __float_as_uint(r) & 0xffu;
-      if (!(fabsf(t - (r - 12582912.f)) <= 0.5f - 0x1p-15f)) c[i] = int8_code(__fdiv_rn(f[i], s));
+      const float lo = fmaf(f[i], inv.lo, 12582912.f), hi = fmaf(f[i], inv.hi, 12582912.f);
+      c[i] = __float_as_uint(hi);
+      if (!(lo == hi)) c[i] = int8_code(__fdiv_rn(f[i], s));
     }
-    out.x = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-    out.y = c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24);
+    const uint32_t a = __byte_perm(c[0], c[1], 0x0040), b = __byte_perm(c[2], c[3], 0x0040);
+    const uint32_t d = __byte_perm(c[4], c[5], 0x0040), e = __byte_perm(c[6], c[7], 0x0040);
+    out.x = __byte_perm(a, b, 0x5410);
+    out.y = __byte_perm(d, e, 0x5410);
   }
   return out;
 }
