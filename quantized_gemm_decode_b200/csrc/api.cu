@@ -1091,7 +1091,7 @@ qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl
   qgd_status st = check_device();
   if (st != QGD_OK) return st;
   RouteArgs a{logits, bias, weights, ids, T, E, ldl, r.top_k, r.score == QGD_SCORE_SIGMOID, r.groups, r.topk_groups,
-              r.group_top, r.renormalize != 0, r.scale, false, false};
+              r.group_top, r.renormalize != 0, r.scale, 0, -1, false, false};
   const cudaError_t e = launch_route(a, logits_dtype == QGD_DTYPE_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_route launch");
 }

@@ -85,9 +85,9 @@ __device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int e) {
 }
 
 __device__ __forceinline__ float warp_max_f(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 // Order-preserving integers (the key 0, below every number's, marks "not a candidate").
@@ -141,11 +141,11 @@ __device__ __forceinline__ typename T::V keep_groups(const RouteArgs& a, int lan
                                                      typename T::K (&key)[kVPT]) {
   using K = typename T::K;
   using V = typename T::V;
-  const int per = a.E / a.groups;
+  const int per = a.per;
   auto group_value = [&](K b1, K b2) -> K { return a.top == 2 && b2 ? T::key(T::value(b1) + T::value(b2)) : b1; };
   K mine = 0;  // lane g: group g's value
-  const int span = per / kVPT;  // lanes of a group, where groups do not share lanes
-  const bool whole_lanes = per % kVPT == 0 && (span & (span - 1)) == 0;
+  const bool whole_lanes = a.span_log >= 0;  // a group is a power of two of whole lanes
+  const int span = 1 << (whole_lanes ? a.span_log : 0);
   if (whole_lanes) {
     K b1 = 0, b2 = 0;
 #pragma unroll
@@ -155,7 +155,7 @@ __device__ __forceinline__ typename T::V keep_groups(const RouteArgs& a, int lan
       merge2<K>(b1, b2, o1, o2);
     }
     const K v = group_value(b1, b2);
-    mine = __shfl_sync(kFull, v, lane * span & 31);
+    mine = __shfl_sync(kFull, v, (lane << a.span_log) & 31);
     if (lane >= a.groups) mine = 0;
   } else {
     for (int g = 0; g < a.groups; ++g) {
@@ -183,7 +183,7 @@ __device__ __forceinline__ typename T::V keep_groups(const RouteArgs& a, int lan
   const bool in = lane < a.groups && rank < a.keep;
   const unsigned kept = __ballot_sync(kFull, in);
   if (whole_lanes) {
-    const bool mine_kept = (kept >> (lane / span & 31)) & 1u;
+    const bool mine_kept = (kept >> (lane >> a.span_log)) & 1u;
 #pragma unroll
     for (int j = 0; j < kVPT; ++j) key[j] = mine_kept ? key[j] : K(0);
   } else {
@@ -222,9 +222,9 @@ __device__ __forceinline__ double exp_series(double x) {
   return p * __hiloint2double((static_cast<int>(n) + 1023) << 20, 0);
 }
 
-// 1 / d to about 2^-46 for d in fp32's range: a 32-bit reciprocal and one Newton step.
+// 1 / d to about 2^-42 for d well inside fp32's range: a 32-bit reciprocal and one Newton step.
 __device__ __forceinline__ double reciprocal(double d) {
-  const double r = static_cast<double>(__frcp_rn(static_cast<float>(d)));
+  const double r = static_cast<double>(__fdividef(1.f, static_cast<float>(d)));
   return fma(r, fma(-d, r, 1.0), r);
 }
 
@@ -318,7 +318,7 @@ __device__ __noinline__ void route_row_exact(const RouteArgs& a, int t, int lane
 constexpr int kRouteWarps = 4;
 
 template <int kVPT, bool kBf16>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, kVPT <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -346,9 +346,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     }
   }
   float mx = -INFINITY;
+  if (!a.sigmoid) {
 #pragma unroll
-  for (int j = 0; j < kVPT; ++j) mx = fmaxf(mx, x[j]);
-  mx = warp_max_f(mx);
+    for (int j = 0; j < kVPT; ++j) mx = fmaxf(mx, x[j]);
+    mx = warp_max_f(mx);
+  }
   const bool grouped = a.keep < a.groups;
   const bool by_score = a.bias != nullptr || (grouped && a.top == 2);  // scores decide something
   const bool need_total = !a.sigmoid && !a.renorm;
@@ -418,20 +420,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     b = key[j] > b ? key[j] : b;
   }
   // The k best and one more; lane i keeps the i-th.
-  int my_id = -1;
-  unsigned my_key = 0u, last_key = 0u;  // last: the one behind the k
+  // (lane i also keeps whose it was; with k = 32 the one behind is kept apart)
+  unsigned my_key = 0u, last_key = 0u;
+  int my_owner = 0;
   const int rounds = sure ? a.k + 1 : 0;
   for (int i = 0; i < rounds; ++i) {
     const unsigned most = warp_max_key(b);
-    if (most == 0u) break;
+    if (most == 0u) {
+      last_key = 0u;
+      break;
+    }
     const int owner = __ffs(__ballot_sync(kFull, (b | kIdx) == (most | kIdx))) - 1;  // the lowest lane of equals
     const unsigned best = __shfl_sync(kFull, b, owner);
-    const int id = owner * kVPT + static_cast<int>(kIdx - (best & kIdx));
-    if (i == a.k) {
-      last_key = best;
-    } else if (lane == i) {
-      my_id = id;
+    last_key = best;
+    if (lane == i) {
       my_key = best;
+      my_owner = owner;
     }
     const unsigned gone = lane == owner ? best : 0xffffffffu;
     b = 0u;
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   // Neighbours in the order must be further apart than their errors (without a
   // bias: than the cut) or equal by construction (same logit, same bias); the
   // first one left out must be apart, since its equals behind it were not seen.
+  const int my_id = lane < a.k && my_key ? my_owner * kVPT + static_cast<int>(kIdx - (my_key & kIdx)) : -1;
   const float my_x = my_id >= 0 ? logit_at<kBf16>(a, t, my_id) : 0.f;
   const float my_b = a.bias && my_id >= 0 ? __ldg(a.bias + my_id) : 0.f;
   if (a.bias || !kBf16) {  // (the cut takes nothing from a bf16 logit: its keys are exact)
@@ -695,6 +700,11 @@ template <int kVPT, bool kBf16>
 cudaError_t launch_route_v(RouteArgs a, cudaStream_t st) {
   const bool whole = a.E % kVPT == 0;
   a.vec = whole && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && static_cast<size_t>(a.ldl) * (kBf16 ? 2 : 4) % 16 == 0;
+  a.per = a.E / a.groups;
+  a.span_log = -1;
+  if (a.per % kVPT == 0)
+    for (int l = 0; l <= 5; ++l)
+      if (a.per == kVPT << l) a.span_log = l;
   a.vec_bias = whole && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
   return launch_pdl(route_kernel<kVPT, kBf16>, static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps),
                     kRouteWarps * 32, 0, st, a);

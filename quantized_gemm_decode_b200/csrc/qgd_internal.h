@@ -152,6 +152,8 @@ struct RouteArgs {
   int top;             // a group's value: its largest choice value (1) or the sum of its two largest (2)
   int renorm;
   float scale;
+  // set by the launcher: experts per group, and log2 of the lanes that hold one (-1: not whole lanes)
+  int per, span_log;
   bool vec, vec_bias;  // rows of logits / the bias can be read 16 bytes at a time (set by the launcher)
 };
 cudaError_t launch_route(const RouteArgs& a, bool bf16, cudaStream_t stream);
