@@ -21,9 +21,8 @@
 // e4m3 weights: 44.5 us per call, of which the weights stream for 40.5 us (6.5
 // TB/s) after 5.5 us of quantizer, hand-over and tile search.  Many: 256-token
 // tiles of CTA pairs, bound by the MMA, whose operands and the copies that refill
-// them share an SM's shared-memory bandwidth (a 256 x 256 x 128 step takes about
-// 700 cycles against 512 of arithmetic): 8192 tokens x 8 of 64 experts, 2048 x
-// 4096 int8 gate / up weights: 2.4 PFLOP/s in the GEMM, 530 us per call.
+// them share an SM's shared-memory bandwidth: 8192 tokens x 8 of 64 experts, 2048 x
+// 4096 int8 gate / up weights: 2.7 PFLOP/s in the GEMM, 490 us per call.
 //
 // Warp roles: warp 0 issues TMA loads, warp 1 owns TMEM and issues MMAs, the
 // groups of four warps behind them drain the accumulator.  Every wait is bounded.
@@ -159,15 +158,15 @@ static_assert(sizeof(Ctl) <= kCtlBytes, "control block too large");
 // 256 weight rows, each CTA holding 128 of them and half of the tokens;
 // kGroups: epilogue groups, which take a tile's 16-token chunks in turn.
 // Shared memory of one CTA (after 1024-byte alignment): ring of kStages x kKps
-// x (128 weight rows + kXRows token rows) x 128 bytes; per epilogue group two
-// output staging buffers of 16 tokens x 128 bf16 (with the activation an
-// exchange area of 8 x 128 floats and one buffer of 16 x 64) and the token
+// x (128 weight rows + kXRows token rows) x 128 bytes; per epilogue group an
+// output staging buffer of 16 tokens x 128 bf16 (with the activation an
+// exchange area of 8 x 128 floats and a buffer of 16 x 64) and the token
 // scales [2][kTok]; control block; running tile counts and first rows of the
 // experts.
 template <int kTok, int kKps, bool kPair, int kGroups, bool kAct>
 struct Layout {
   static constexpr int kThreads = 64 + kGroups * kEpiThreads;
-  static constexpr uint32_t kOut = kAct ? 8 * kEpiThreads * 4 + 16 * 128 : 2 * 16 * 256;
+  static constexpr uint32_t kOut = kAct ? 8 * kEpiThreads * 4 + 16 * 128 : 16 * 256;
   static constexpr uint32_t kGroupBytes = kOut + 2 * kTok * 4;
   static constexpr int kXRows = kPair ? kTok / 2 : kTok;
   static constexpr int kRound = kPair ? 32 : 16;  // tokens of a tile are rounded up to this
@@ -184,39 +183,10 @@ struct Layout {
   static constexpr size_t kBytes = 1024 + static_cast<size_t>(kStages) * kStage + kTail;
 };
 
-// Where a tile lies: its expert, first sorted row, row count and weight tile.
-struct Tile {
-  int e, row0, n, nt;
-};
-
 // First sorted row of expert e.
 __device__ __forceinline__ int offset_of(const ExpertArgs& a, int e) {
   const int v = __ldg(a.offsets + e);
   return v < 0 ? 0 : (v > a.P ? a.P : v);
-}
-
-// Tile w of the list: weight tiles fastest, then an expert's token tiles, then
-// the experts (pre[e]: token tiles of the experts before e).  An expert's rows
-// are dealt to its token tiles evenly, in multiples of kRound.
-template <int kRound>
-__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const int* pre, const int* off, int n_tiles, int w) {
-  Tile t;
-  const int g = w / n_tiles;
-  t.nt = w - g * n_tiles;
-  int lo = 0, hi = a.E;  // pre[lo] <= g < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= g) lo = mid;
-    else hi = mid;
-  }
-  t.e = lo;
-  const int o0 = off[lo];
-  const int cnt = off[lo + 1] - o0, tiles = pre[lo + 1] - pre[lo];
-  const int per = ((cnt + tiles - 1) / tiles + kRound - 1) & ~(kRound - 1);
-  const int j = g - pre[lo];
-  t.row0 = o0 + j * per;
-  t.n = min(per, cnt - j * per);
-  return t;
 }
 
 // A worker's (CTA's or CTA pair's) work as a sequence of segments (tile, K
@@ -242,34 +212,89 @@ struct Deal {
   }
 };
 
+// A segment of a tile: the tile's number, expert, first sorted row, row count and
+// weight tile, and the K units [k0, k1).
+struct Tile {
+  int w, e, row0, n, nt, k0, k1;
+};
+
+// A worker's segments in order.  Tiles are numbered weight tiles fastest, then an
+// expert's token tiles, then the experts (pre[e]: token tiles of the experts
+// before e; off[e]: first sorted row); an expert's rows are dealt to its token
+// tiles evenly, in multiples of kRound.  The walk goes on from the expert it is
+// at: a search and three divisions per tile took the MMA thread 2000 cycles
+// between tiles, as much as four K slices' work.
+template <int kRound>
 struct Walk {
-  int w, k, left, step, nku;  // next segment's tile and first unit; split: units left, else tiles to go
+  const int *pre, *off;
+  int n_tiles, nku, step, step_g, step_nt;
   bool split;
-  __device__ __forceinline__ Walk(const Deal& d, int worker) : step(d.G), nku(d.nku), split(d.split) {
+  int w, k, left;  // next segment's tile and first unit; split: units left, else tiles to go
+  int g, nt;       // the tile's token tile (over all experts) and weight tile
+  int e, lo, hi;   // its expert and that one's token tiles [lo, hi)
+  int first, cnt, per;
+  __device__ __forceinline__ Walk(const Deal& d, const int* pre_, const int* off_, int E, int n_tiles_, int worker)
+      : pre(pre_), off(off_), n_tiles(n_tiles_), nku(d.nku), step(d.G), split(d.split) {
     if (split) {
       const int u = d.begin(worker);
       w = u / nku;
       k = u - w * nku;
       left = d.q + (worker < d.r ? 1 : 0);
+      step = 1;
     } else {
       w = worker;
       k = 0;
       left = d.total - worker;
     }
+    step_g = step / n_tiles;
+    step_nt = step - step_g * n_tiles;
+    g = w / n_tiles;
+    nt = w - g * n_tiles;
+    int a = 0, b = E;  // pre[a] <= g < pre[b], where there is such a tile
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (pre[mid] <= g) a = mid;
+      else b = mid;
+    }
+    if (left > 0) enter(a);
   }
-  __device__ __forceinline__ bool next(int& tile, int& k0, int& k1) {
+  __device__ __forceinline__ void enter(int expert) {
+    e = expert;
+    lo = pre[e];
+    hi = pre[e + 1];
+    first = off[e];
+    cnt = off[e + 1] - first;
+    const int tiles = hi - lo;
+    per = tiles > 0 ? ((cnt + tiles - 1) / tiles + kRound - 1) & ~(kRound - 1) : 0;
+  }
+  __device__ __forceinline__ bool next(Tile& t) {
     if (left <= 0) return false;
-    tile = w;
-    k0 = k;
-    k1 = nku;
+    if (g >= hi) {
+      int x = e + 1;
+      while (pre[x + 1] <= g) ++x;
+      enter(x);
+    }
+    const int at = (g - lo) * per;
+    t.w = w;
+    t.e = e;
+    t.row0 = first + at;
+    t.n = min(per, cnt - at);
+    t.nt = nt;
+    t.k0 = k;
+    t.k1 = nku;
     if (split) {
-      if (left < nku - k) k1 = k + left;
-      left -= k1 - k0;
-      ++w;
+      if (left < nku - k) t.k1 = k + left;
+      left -= t.k1 - t.k0;
       k = 0;
     } else {
-      w += step;
       left -= step;
+    }
+    w += step;
+    g += step_g;
+    nt += step_nt;
+    if (nt >= n_tiles) {
+      nt -= n_tiles;
+      ++g;
     }
     return true;
   }
@@ -365,12 +390,11 @@ __device__ __forceinline__ uint32_t add_acc(uint32_t x, uint32_t y) {
 // one column.  With the activation the first two warps hold 64 gate rows and
 // the last two their up rows: two threads of one column swap halves through
 // shared memory, the gate's finishing the even tokens, the up's the odd ones.
-// `out`: exchange area (activation only) and staging, see Layout.  Without the
-// activation staging alternates between two buffers; with it the exchange's
-// barrier already keeps a chunk's stores ahead of the next chunk's values.
+// `out`: exchange area (activation only) and staging, see Layout; the first
+// barrier of a chunk is also behind the stores of the chunk before.
 template <int kFmt, bool kAct>
 __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, const uint32_t (&r)[16], int c0, float swv,
-                                         const float* sxs, uint8_t* out, int group, uint32_t& flip) {
+                                         const float* sxs, uint8_t* out, int group) {
   const int et = (threadIdx.x - 64) & (kEpiThreads - 1), lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
   float v[16];
 #pragma unroll
@@ -404,8 +428,8 @@ __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, con
     for (int j = 0; j < 8; ++j)
       buf[(2 * j + (up ? 1 : 0)) * 64 + (row & 63)] = __bfloat16_as_ushort(__float2bfloat16_rn(h[j]));
   } else {
-    buf = reinterpret_cast<uint16_t*>(out + (flip & 1u) * (16 * 256));
-    flip ^= 1u;
+    buf = reinterpret_cast<uint16_t*>(out);
+    epi_sync(group);
 #pragma unroll
     for (int j = 0; j < 16; ++j) buf[j * 128 + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
   }
@@ -544,11 +568,11 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     if (lane == 0 && busy) {
       const uint64_t pol_w = kSplit ? policy_evict_first() : policy_evict_last();
       const uint64_t pol_x = policy_evict_last();
-      Walk walk(deal, me);
-      int w, k0, k1, i = 0;
+      Walk<L::kRound> walk(deal, pre, off, a.E, n_tiles, me);
+      Tile t;
+      int i = 0;
       bool stop = false;
-      while (!stop && walk.next(w, k0, k1)) {
-        const Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
+      while (!stop && walk.next(t)) {
         const int wt = kPair ? t.nt * 2 + static_cast<int>(rank) : t.nt;  // this CTA's 128 weight rows
         const int all = (t.n + L::kRound - 1) & ~(L::kRound - 1);
         const int mine = kPair ? all / 2 : all;  // token rows in this CTA's shared memory
@@ -556,7 +580,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
         const bool few = mine <= L::kBoxShort;   // rows past the tile's go unused
         const CUtensorMap* xmap = few ? &tx_short : &tx;
         const uint32_t bytes = L::kW + (few ? L::kBoxShort : L::kBoxLong) * kTileK;
-        for (int k = k0; k < k1; ++k, ++i) {
+        for (int k = t.k0; k < t.k1; ++k, ++i) {
           const int s = i % stages;
           if (!mbar_wait(&ctl->empty[s], ((i / stages) & 1) ^ 1)) {
             fail(kErrWaitProducer);
@@ -587,11 +611,11 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     // ---------------- MMA issuer (of a pair: the leader's) ----------------
     if (lane == 0 && rank == 0 && busy) {
       const uint32_t w_base = smem_u32(w_ring), x_base = smem_u32(x_ring);
-      Walk walk(deal, me);
-      int w, k0, k1, i = 0, li = 0;
+      Walk<L::kRound> walk(deal, pre, off, a.E, n_tiles, me);
+      Tile t;
+      int i = 0, li = 0;
       bool stop = false;
-      while (!stop && walk.next(w, k0, k1)) {
-        const Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
+      while (!stop && walk.next(t)) {
         const uint32_t idesc = idesc_mma(kInt ? 2 : 1, kInt ? 1 : 0, (kPair ? 2 : 1) * kSwapTileN,
                                          (t.n + L::kRound - 1) & ~(L::kRound - 1));
         const int b = li & 1;
@@ -601,14 +625,10 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
         }
         tc_fence_after();
         const uint32_t d = tmem + b * kTok;
-        for (int k = k0; k < k1; ++k, ++i) {
+        for (int k = t.k0; k < t.k1; ++k, ++i) {
           const int s = i % stages;
           if (!mbar_wait(&ctl->full[s], (i / stages) & 1)) {
             fail(kErrWaitMma);
-            stop = true;
-            break;
-          }
-          if (aborted()) {
             stop = true;
             break;
           }
@@ -619,7 +639,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
             for (int kk = 0; kk < kTileK / 32; ++kk) {
               const uint64_t ad = sdesc_kmajor_sw128(w_base + (s * kKps + h) * L::kW + kk * 32);
               const uint64_t bd = sdesc_kmajor_sw128(x_base + (s * kKps + h) * L::kX + kk * 32);
-              const uint32_t acc = (k > k0 || h > 0 || kk > 0) ? 1u : 0u;
+              const uint32_t acc = (k > t.k0 || h > 0 || kk > 0) ? 1u : 0u;
               if constexpr (kPair) mma_issue_pair<kInt>(d, ad, bd, idesc, acc);
               else mma_issue<kInt>(d, ad, bd, idesc, acc);
             }
@@ -642,24 +662,43 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int lrow = q * 32 + lane;  // row of the weight tile
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
-    Walk walk(deal, me);
-    int w, k0, k1, li = 0;
-    uint32_t flip = 0;
-    while (walk.next(w, k0, k1)) {
-      Tile t = find_tile<L::kRound>(a, pre, off, n_tiles, w);
-      if constexpr (kPair) t.nt = t.nt * 2 + static_cast<int>(rank);
-      const int b = li & 1;
-      float* sxs = sx_s + b * kTok;
-      for (int i = et; i < ((t.n + 15) & ~15); i += kEpiThreads) sxs[i] = i < t.n ? __ldg(a.sx + t.row0 + i) : 0.f;
-      // this thread's weight row and its channel scale (0 past the last row)
-      float swv = 0.f;
+    // A tile's token scales and this thread's channel scale are loaded while the
+    // tile before is finished.
+    constexpr int kPerThread = (kTok + kEpiThreads - 1) / kEpiThreads;
+    float sx_next[kPerThread], sw_next = 0.f;
+    auto prefetch = [&](const Tile& t) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        const int r = i * kEpiThreads + et;
+        sx_next[i] = r < t.n ? __ldg(a.sx + t.row0 + r) : 0.f;
+      }
+      // the thread's weight row (0 past the last row)
+      sw_next = 0.f;
       if constexpr (kAct) {
         const int col = t.nt * 64 + (lrow & 63);
-        if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * 2 * a.N + (lrow >= 64 ? a.N : 0) + col);
+        if (col < a.N) sw_next = __ldg(a.sw + static_cast<size_t>(t.e) * 2 * a.N + (lrow >= 64 ? a.N : 0) + col);
       } else {
         const int col = t.nt * 128 + lrow;
-        if (col < a.N) swv = __ldg(a.sw + static_cast<size_t>(t.e) * a.N + col);
+        if (col < a.N) sw_next = __ldg(a.sw + static_cast<size_t>(t.e) * a.N + col);
       }
+    };
+    Walk<L::kRound> walk(deal, pre, off, a.E, n_tiles, me);
+    auto next_tile = [&](Tile& t) {
+      if (!walk.next(t)) return false;
+      if constexpr (kPair) t.nt = t.nt * 2 + static_cast<int>(rank);
+      prefetch(t);
+      return true;
+    };
+    Tile t, coming;
+    int li = 0;
+    for (bool more = next_tile(t); more; t = coming, ++li) {
+      const int b = li & 1;
+      float* sxs = sx_s + b * kTok;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (i * kEpiThreads + et < kTok) sxs[i * kEpiThreads + et] = sx_next[i];
+      const float swv = sw_next;
+      more = next_tile(coming);
       const bool ok = warp_wait(&ctl->tfull[b], (li >> 1) & 1);
       if (!ok && lane == 0) fail(kErrWaitEpilogue);
       if (ok) tc_fence_after();
@@ -672,12 +711,12 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       if constexpr (kSplit) all_groups_sync<kGroups>();
       else epi_sync(group);
       if (!ctl->epi_ok[table]) break;
-      const bool whole = !kSplit || !split || (k0 == 0 && k1 == nku);
+      const bool whole = !kSplit || !split || (t.k0 == 0 && t.k1 == nku);
       int first = me, ncontrib = 1;
       uint32_t* slot = nullptr;
       if (!whole) {
-        first = deal.owner(w * nku);
-        ncontrib = deal.owner(w * nku + nku - 1) - first + 1;
+        first = deal.owner(t.w * nku);
+        ncontrib = deal.owner(t.w * nku + nku - 1) - first + 1;
         slot = a.partial + (static_cast<size_t>(me) * 2 + (me == first ? 1 : 0)) * (kSwapTileN * kTok) + lrow;
       }
       const int chunks = (t.n + 15) >> 4;
@@ -697,7 +736,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
         tmem_wait_ld();
         if (c + kGroups >= chunks) release();
         if (whole) {
-          finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, group, flip);
+          finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, group);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) __stcg(slot + (c * 16 + j) * kSwapTileN, r[j]);
@@ -724,11 +763,10 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
 #pragma unroll
               for (int m = 0; m < 16; ++m) sum[m] = j == 0 ? v[m] : add_acc<kFmt>(sum[m], v[m]);
             }
-            finish16<kFmt, kAct>(a, t, sum, c * 16, swv, sxs, out, group, flip);
+            finish16<kFmt, kAct>(a, t, sum, c * 16, swv, sxs, out, group);
           }
         }
       }
-      ++li;
     }
   }
 
@@ -867,7 +905,7 @@ cudaError_t launch_f(const CUtensorMap& tw, const CUtensorMap& tx, const CUtenso
   switch (a.tok) {
     case 64: return launch_t<kFmt, 64, 2, true, false, 2, kAct>(tw, tx, tx_short, a, st);
     case 128: return launch_t<kFmt, 128, 2, true, false, 2, kAct>(tw, tx, tx_short, a, st);
-    case 256: return launch_t<kFmt, 256, 1, false, true, 3, kAct>(tw, tx, tx_short, a, st);
+    case 256: return launch_t<kFmt, 256, 2, false, true, 3, kAct>(tw, tx, tx_short, a, st);
   }
   return cudaErrorInvalidValue;
 }
