@@ -766,15 +766,15 @@ ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
 }
 
 // Expert weights [E][rows][K] as boxes of 128 bytes x 128 rows, or with the
-// gated activation [E][2][N][K] as 128 bytes x 64 gate rows and their 64 up
-// rows; 128-byte swizzle, zeros past the extents.
+// gated activation [E][2][N][K] as 128 bytes x 8 x (8 gate rows, their 8 up
+// rows); 128-byte swizzle, zeros past the extents.
 qgd_status encode_experts(CUtensorMap* map, const void* base, int E, int N, int K, bool act) {
   const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), e = static_cast<cuuint64_t>(E);
-  cuuint64_t dims[4] = {k, n, act ? 2 : e, e};
-  cuuint64_t strides[3] = {k, k * n, 2 * k * n};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(kTileK), act ? 64u : 128u, act ? 2u : 1u, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, act ? 4 : 3, const_cast<void*>(base), dims, strides, box,
+  cuuint64_t dims[5] = {k, act ? 8 : n, act ? 2 : e, n / 8, e};
+  cuuint64_t strides[4] = {k, k * n, 8 * k, 2 * k * n};
+  cuuint32_t box[5] = {static_cast<cuuint32_t>(kTileK), act ? 8u : 128u, act ? 2u : 1u, 8, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, act ? 5 : 3, const_cast<void*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
@@ -1143,7 +1143,11 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   if (order && top_k < 1) return fail(QGD_ERR_INVALID, "top_k=%d must be positive", top_k);
   if (!order && rows > x_rows) return fail(QGD_ERR_INVALID, "%d rows of %d without an order", rows, x_rows);
   const long long n_all = static_cast<long long>(N) * (act == QGD_ACT_SILU_MUL ? 2 : 1);
-  if (n_all * E >= (1LL << 30) || (static_cast<long long>(rows) / 64 + E) * ((N + 63) / 64) > (1LL << 31) - 1)
+  // (the kernel counts tiles, and tiles x K steps, in 32 bits; its running tile
+  // counts stay there whatever the offsets hold)
+  const long long token_tiles = rows / 64;
+  if (n_all * E >= (1LL << 30) || (token_tiles + E) * ((N + 63) / 64) * ((K + 255) / 256) >= (1LL << 31) ||
+      (token_tiles + 1) * E >= (1LL << 31))
     return fail(QGD_ERR_UNSUPPORTED, "too many weight rows or tiles (rows=%d E=%d N=%d)", rows, E, N);
   if (rows == 0) return QGD_OK;
   if (x_rows == 0) return fail(QGD_ERR_INVALID, "%d rows of an empty x", rows);

@@ -156,17 +156,17 @@ static_assert(sizeof(Ctl) <= kCtlBytes, "control block too large");
 
 // Shapes of a variant.  kTok: most tokens per tile; kPair: a CTA pair computes
 // 256 weight rows, each CTA holding 128 of them and half of the tokens;
-// kGroups: epilogue groups, which take a tile's 16-token chunks in turn.
+// kGroups: epilogue groups, which take a tile's 16-token chunks in turn; kAct: a
+// tile's 128 weight rows are 8 gate rows, their 8 up rows, the next 8 gate rows, ...
 // Shared memory of one CTA (after 1024-byte alignment): ring of kStages x kKps
 // x (128 weight rows + kXRows token rows) x 128 bytes; per epilogue group an
-// output staging buffer of 16 tokens x 128 bf16 (with the activation an
-// exchange area of 8 x 128 floats and a buffer of 16 x 64) and the token
-// scales [2][kTok]; control block; running tile counts and first rows of the
+// output staging buffer of 16 tokens x 128 bf16 (with the activation 16 x 64) and
+// the token scales [2][kTok]; control block; running tile counts and first rows of the
 // experts.
 template <int kTok, int kKps, bool kPair, int kGroups, bool kAct>
 struct Layout {
   static constexpr int kThreads = 64 + kGroups * kEpiThreads;
-  static constexpr uint32_t kOut = kAct ? 8 * kEpiThreads * 4 + 16 * 128 : 16 * 256;
+  static constexpr uint32_t kOut = kAct ? 16 * 128 : 16 * 256;
   static constexpr uint32_t kGroupBytes = kOut + 2 * kTok * 4;
   static constexpr int kXRows = kPair ? kTok / 2 : kTok;
   static constexpr int kRound = kPair ? 32 : 16;  // tokens of a tile are rounded up to this
@@ -342,20 +342,21 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// Gate and up rows, 8 and 8: dimensions K, row of 8, gate / up, block of 8 rows, expert.
 template <bool kPair>
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                            int v, uint64_t policy) {
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int block, int e,
+                                            uint64_t policy) {
   if constexpr (kPair)
     asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "l"(policy)
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(0), "r"(block), "r"(e), "l"(policy)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "l"(policy)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(0), "r"(block), "r"(e), "l"(policy)
         : "memory");
 }
 
@@ -383,67 +384,89 @@ __device__ __forceinline__ uint32_t add_acc(uint32_t x, uint32_t y) {
   else return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
 }
 
-// Sixteen tokens of this thread's weight row, finished and stored.  r: the
-// accumulators of tokens c0 .. c0 + 15 of the tile.  The group's warps write
-// bf16 rows [token][column] to shared memory and then store whole 16-byte
-// vectors, so that y leaves in 128- or 256-byte runs although a thread holds
-// one column.  With the activation the first two warps hold 64 gate rows and
-// the last two their up rows: two threads of one column swap halves through
-// shared memory, the gate's finishing the even tokens, the up's the odd ones.
-// `out`: exchange area (activation only) and staging, see Layout; the first
-// barrier of a chunk is also behind the stores of the chunk before.
+// A 16-token chunk of the accumulator as 8 x 8 fragments: r[8h + 4g + 2x + i] is
+// lane 16h + 8x + l / 4 of the warp's 32, token 8g + 2(l % 4) + i (l: the thread's
+// lane).  So a gate row and its up row, 8 lanes on, meet in one thread, and two
+// tokens of a channel pack into the register that a transposing matrix store takes.
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane 8m + j gives the address
+// of row j of matrix m.
+__device__ __forceinline__ void store_matrices_t(uint32_t addr, const uint32_t (&m)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(m[0]),
+               "r"(m[1]), "r"(m[2]), "r"(m[3])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A chunk's accumulators (see load_chunk) finished and stored: tokens c0 .. c0 + 15
+// of the tile.  sw: scales of the thread's rows, sw[2h + x].  The group's warps
+// write [token][channel] to shared memory, 8 channels of a token at a time, the
+// 16-byte vectors of a token swapped by its low three bits (no bank conflicts), and
+// store y from there in runs of 128 or 256 bytes.  The operands' stream through
+// shared memory bounds the large tiles, so the epilogue has to use little of it:
+// with a row per thread, gate and up swapped through shared memory and 2-byte
+// stores it took four times as many accesses.
 template <int kFmt, bool kAct>
-__device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, const uint32_t (&r)[16], int c0, float swv,
-                                         const float* sxs, uint8_t* out, int group) {
+__device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, const uint32_t (&r)[16], int c0,
+                                         const float (&sw)[4], const float* sxs, uint8_t* out, int group) {
   const int et = (threadIdx.x - 64) & (kEpiThreads - 1), lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
-  float v[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 f = *reinterpret_cast<const float4*>(sxs + c0 + 4 * j);
-    v[4 * j] = (acc_value<kFmt>(r[4 * j]) * f.x) * swv;
-    v[4 * j + 1] = (acc_value<kFmt>(r[4 * j + 1]) * f.y) * swv;
-    v[4 * j + 2] = (acc_value<kFmt>(r[4 * j + 2]) * f.z) * swv;
-    v[4 * j + 3] = (acc_value<kFmt>(r[4 * j + 3]) * f.w) * swv;
-  }
-  uint16_t* buf;
-  if constexpr (kAct) {
-    float* swap = reinterpret_cast<float*>(out);
-    buf = reinterpret_cast<uint16_t*>(out + 8 * kEpiThreads * 4);
-    const bool up = q >= 2;
-    const int row = q * 32 + lane;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) swap[j * kEpiThreads + row] = up ? v[2 * j] : v[2 * j + 1];
-    epi_sync(group);
-    // (all loads before the first store: the compiler must take them for one
-    // memory, and one value after the other cost 1050 cycles a chunk)
-    float other[8], h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) other[j] = swap[j * kEpiThreads + (row ^ 64)];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float gate = up ? other[j] : v[2 * j], lin = up ? v[2 * j + 1] : other[j];
-      h[j] = silu(gate) * lin;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      buf[(2 * j + (up ? 1 : 0)) * 64 + (row & 63)] = __bfloat16_as_ushort(__float2bfloat16_rn(h[j]));
-  } else {
-    buf = reinterpret_cast<uint16_t*>(out);
-    epi_sync(group);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) buf[j * 128 + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
-  }
-  epi_sync(group);
   constexpr int kCols = kAct ? 64 : 128;
   constexpr int kVecs = kCols / 8;  // 16-byte vectors per token
+  uint32_t m[kAct ? 1 : 2][4];
+  float v[16];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float2 sx = *reinterpret_cast<const float2*>(sxs + c0 + 8 * g + 2 * (lane & 3));
+#pragma unroll
+    for (int hx = 0; hx < 4; ++hx) {
+      const int at = 8 * (hx >> 1) + 4 * g + 2 * (hx & 1);
+      v[at] = (acc_value<kFmt>(r[at]) * sx.x) * sw[hx];
+      v[at + 1] = (acc_value<kFmt>(r[at + 1]) * sx.y) * sw[hx];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = 8 * h + 4 * g;
+      if constexpr (kAct) {
+        m[0][2 * h + g] = pack_bf16(silu(v[at]) * v[at + 2], silu(v[at + 1]) * v[at + 3]);
+      } else {
+        m[h][g] = pack_bf16(v[at], v[at + 1]);
+        m[h][2 + g] = pack_bf16(v[at + 2], v[at + 3]);
+      }
+    }
+  }
+  // this lane's row: token 8 (lane / 8 % 2) + lane % 8, vector by q, h or x (lane / 16) and the store
+  const int tok = lane & 15;
+  const uint32_t row = smem_u32(out) + tok * (kCols * 2);
+  epi_sync(group);  // the chunk before has left the buffer
+  if constexpr (kAct) {
+    store_matrices_t(row + (((q * 2 + (lane >> 4)) ^ (tok & 7)) << 4), m[0]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store_matrices_t(row + (((q * 4 + h * 2 + (lane >> 4)) ^ (tok & 7)) << 4), m[h]);
+  }
+  epi_sync(group);
 #pragma unroll
   for (int p = 0; p < 16 * kVecs / kEpiThreads; ++p) {
     const int idx = p * kEpiThreads + et;
-    const int tok = idx / kVecs, vec = idx - tok * kVecs;
+    const int tk = idx / kVecs, vec = idx - tk * kVecs;
     const int col = t.nt * kCols + vec * 8;
-    if (c0 + tok < t.n && col < a.N)
-      *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(t.row0 + c0 + tok) * a.N + col) =
-          *reinterpret_cast<const uint4*>(buf + tok * kCols + vec * 8);
+    if (c0 + tk < t.n && col < a.N)
+      *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(t.row0 + c0 + tk) * a.N + col) =
+          *reinterpret_cast<const uint4*>(out + tk * (kCols * 2) + ((vec ^ (tk & 7)) << 4));
   }
 }
 
@@ -537,8 +560,10 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const int n_tiles = kPair ? (a.n_tiles + 1) / 2 : a.n_tiles;
-  const int total = pre[a.E] * n_tiles;
-  const int U = total * nku;  // (below 2^31: the host checks)
+  // (no tiles where offsets that do not ascend list rows over and over: the host's
+  // check of the sizes, which keeps these numbers below 2^31, holds for ascending ones)
+  const int total = pre[a.E] <= a.P / kTok + a.E ? pre[a.E] * n_tiles : 0;
+  const int U = total * nku;
   const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
   // Whole tiles leave workers idle at the end, split ones cost a hand-over (about
   // 3 us: partials, arrival, sum); a K unit of 32 KB takes an SM's share of the
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
           for (int h = 0; h < ns; ++h) {
             const int x = (kt + h) * kTileK;
             uint8_t* wd = w_ring + (s * kKps + h) * L::kW;
-            if constexpr (kAct) tma_load_4d<kPair>(wd, &tw, fb, x, wt * 64, 0, t.e, pol_w);  // 64 gate rows, their up rows
+            if constexpr (kAct) tma_load_5d<kPair>(wd, &tw, fb, x, wt * 8, t.e, pol_w);
             else tma_load_3d<kPair>(wd, &tw, fb, x, wt * 128, t.e, pol_w);
             tma_load_rows<kPair>(x_ring + (s * kKps + h) * L::kX, xmap, &ctl->full[s], fb, x, xrow, pol_x);
           }
@@ -660,27 +685,21 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     uint8_t* out = groups + group * L::kGroupBytes;
     float* sx_s = reinterpret_cast<float*>(out + L::kOut);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const int lrow = q * 32 + lane;  // row of the weight tile
+    const int lrow = q * 32 + lane;
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u;
-    // A tile's token scales and this thread's channel scale are loaded while the
+    // A tile's token scales and the scale of the row at this thread's lane are loaded while the
     // tile before is finished.
     constexpr int kPerThread = (kTok + kEpiThreads - 1) / kEpiThreads;
-    float sx_next[kPerThread], sw_next = 0.f;
+    float sx_next[kPerThread], sw_next;
     auto prefetch = [&](const Tile& t) {
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i) {
         const int r = i * kEpiThreads + et;
         sx_next[i] = r < t.n ? __ldg(a.sx + t.row0 + r) : 0.f;
       }
-      // the thread's weight row (0 past the last row)
-      sw_next = 0.f;
-      if constexpr (kAct) {
-        const int col = t.nt * 64 + (lrow & 63);
-        if (col < a.N) sw_next = __ldg(a.sw + static_cast<size_t>(t.e) * 2 * a.N + (lrow >= 64 ? a.N : 0) + col);
-      } else {
-        const int col = t.nt * 128 + lrow;
-        if (col < a.N) sw_next = __ldg(a.sw + static_cast<size_t>(t.e) * a.N + col);
-      }
+      const int col = kAct ? t.nt * 64 + (lrow >> 4) * 8 + (lane & 7) : t.nt * 128 + lrow;
+      const size_t from = kAct ? (static_cast<size_t>(t.e) * 2 + (lane >> 3 & 1)) * a.N : static_cast<size_t>(t.e) * a.N;
+      sw_next = col < a.N ? __ldg(a.sw + from + col) : 0.f;  // (0 past the last row)
     };
     Walk<L::kRound> walk(deal, pre, off, a.E, n_tiles, me);
     auto next_tile = [&](Tile& t) {
@@ -697,7 +716,9 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
         if (i * kEpiThreads + et < kTok) sxs[i * kEpiThreads + et] = sx_next[i];
-      const float swv = sw_next;
+      float sw[4];
+#pragma unroll
+      for (int hx = 0; hx < 4; ++hx) sw[hx] = __shfl_sync(0xffffffffu, sw_next, 8 * hx + (lane >> 2));
       more = next_tile(coming);
       const bool ok = warp_wait(&ctl->tfull[b], (li >> 1) & 1);
       if (!ok && lane == 0) fail(kErrWaitEpilogue);
@@ -732,11 +753,10 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
       for (int c = group; c < chunks; c += kGroups) {
         uint32_t r[16];
         __syncwarp();
-        tmem_ld16(taddr + b * kTok + c * 16, r);
-        tmem_wait_ld();
+        load_chunk(taddr + b * kTok + c * 16, r);
         if (c + kGroups >= chunks) release();
         if (whole) {
-          finish16<kFmt, kAct>(a, t, r, c * 16, swv, sxs, out, group);
+          finish16<kFmt, kAct>(a, t, r, c * 16, sw, sxs, out, group);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) __stcg(slot + (c * 16 + j) * kSwapTileN, r[j]);
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
 #pragma unroll
               for (int m = 0; m < 16; ++m) sum[m] = j == 0 ? v[m] : add_acc<kFmt>(sum[m], v[m]);
             }
-            finish16<kFmt, kAct>(a, t, sum, c * 16, swv, sxs, out, group);
+            finish16<kFmt, kAct>(a, t, sum, c * 16, sw, sxs, out, group);
           }
         }
       }

@@ -63,7 +63,8 @@ def test_sort_refusals(kw, status):
     (dict(rows=-1), -1), (dict(N=24), -2), (dict(N=0), -1), (dict(K=40), -2), (dict(K=16400, ldx=16400), -2),
     (dict(E=0), -1), (dict(E=2000), -2), (dict(ldx=56), -1), (dict(ldx=68), -1), (dict(top_k=0), -1),
     (dict(order=None, rows=9), -1), (dict(x_rows=0), -1), (dict(x=None), -1), (dict(wq=P((1 << 20) + 8)), -1), (dict(y=P((1 << 20) + 8)), -1),
-    (dict(sw=P((1 << 20) + 2)), -1), (dict(offsets=None), -1), (dict(N=1 << 20, E=1024), -2), (dict(rows=0), 0)])
+    (dict(sw=P((1 << 20) + 2)), -1), (dict(offsets=None), -1), (dict(N=1 << 20, E=1024), -2), (dict(rows=0), 0),
+    (dict(rows=1 << 28, E=1024, N=16), -2), (dict(rows=1 << 28, N=4096, K=16384, ldx=16384), -2)])
 def test_experts_refusals(kw, status):
     d = dict(fmt=1, x=A, ldx=64, x_rows=8, order=A, top_k=2, offsets=A, E=4, rows=16, wq=A, sw=A, y=A, N=32, K=64, act=0,
              ws=A, ws_bytes=1 << 40)
