@@ -18,11 +18,11 @@
 // Few rows per expert: 64- or 128-token tiles, bound by the one pass over the
 // weights; (tile, K unit) units are dealt out over all SMs where whole tiles would
 // leave too many idle.  Measured on B200, 32 tokens x 8 of 64 experts, 4096 x 1024
-// e4m3 weights: 44.5 us per call, of which the weights stream for 40.5 us (6.5
+// e4m3 weights: 44.2 us per call, of which the weights stream for 40.5 us (6.5
 // TB/s) after 5.5 us of quantizer, hand-over and tile search.  Many: 256-token
 // tiles of CTA pairs, bound by the MMA, whose operands and the copies that refill
 // them share an SM's shared-memory bandwidth: 8192 tokens x 8 of 64 experts, 2048 x
-// 4096 int8 gate / up weights: 2.7 PFLOP/s in the GEMM, 490 us per call.
+// 4096 int8 gate / up weights: 2.8 PFLOP/s in the GEMM, 484 us per call.
 //
 // Warp roles: warp 0 issues TMA loads, warp 1 owns TMEM and issues MMAs, the
 // groups of four warps behind them drain the accumulator.  Every wait is bounded.
@@ -419,7 +419,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // store y from there in runs of 128 or 256 bytes.  The operands' stream through
 // shared memory bounds the large tiles, so the epilogue has to use little of it:
 // with a row per thread, gate and up swapped through shared memory and 2-byte
-// stores it took four times as many accesses.
+// stores it took three times as many accesses.
 template <int kFmt, bool kAct>
 __device__ __forceinline__ void finish16(const ExpertArgs& a, const Tile& t, const uint32_t (&r)[16], int c0,
                                          const float (&sw)[4], const float* sxs, uint8_t* out, int group) {
