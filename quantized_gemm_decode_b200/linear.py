@@ -129,7 +129,8 @@ class QuantizedExperts:
 
     A call up to GRAPH_MAX_M tokens replays the graph of its bucket once
     capture() has run (rows behind the call's tokens are padding, routed to no
-    expert); other calls launch directly.  Direct calls may overlap (other
+    expert); other calls, and those with logits of another type than the
+    graph's, launch directly.  Direct calls may overlap (other
     streams); a captured bucket's buffers are shared by its replays, which
     must not."""
 
@@ -155,11 +156,14 @@ class QuantizedExperts:
         wq, sw = qgd.quant_weight_per_channel(w.reshape(E * rows, K), qt)
         return wq.view(E, rows, K), sw.view(E, rows)
 
+    def _check(self, x, logits) -> None:
+        if x.shape != (logits.shape[0], self.H) or logits.shape != (x.shape[0], self.E):
+            raise ValueError(f"x {tuple(x.shape)} and logits {tuple(logits.shape)} for {self.E} experts of width {self.H}")
+
     def layer(self, x: torch.Tensor, logits: torch.Tensor, add=None, y=None) -> torch.Tensor:
         """The layer on x [T, H] bf16 and logits [T, E] (bf16 or fp32), on the
         current stream; either may be a column slice of a wider matrix."""
-        if x.shape[0] != logits.shape[0] or logits.shape[1] != self.E or x.shape[1] != self.H:
-            raise ValueError(f"x {tuple(x.shape)} and logits {tuple(logits.shape)} for {self.E} experts of width {self.H}")
+        self._check(x, logits)
         w, ids = qgd.moe_route(logits, self.top_k, **self.route)
         offsets, order, pos = qgd.moe_sort(ids, self.E)
         h = qgd.qlinear_experts_bf16(self.fmt_id, x, self.gate_up, self.gate_up_s, offsets, order=order,
@@ -187,9 +191,14 @@ class QuantizedExperts:
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, add=None) -> torch.Tensor:
         M = x.shape[0]
         mb = qgd.qgd_m_bucket(M) if 0 < M <= GRAPH_MAX_M else 0
-        if mb not in self._graphs:
+        captured = self._graphs.get(mb)
+        if captured is None or logits.dtype != captured[2].dtype:
             return self.layer(x, logits, add=add)
-        g, xs, ls, adds, ys = self._graphs[mb]
+        g, xs, ls, adds, ys = captured
+        # (a copy into the graph's buffers would broadcast or convert what a direct call refuses)
+        self._check(x, logits)
+        if x.dtype != torch.bfloat16 or (add is not None and (add.dtype != torch.bfloat16 or add.shape != x.shape)):
+            raise ValueError("x and add must be bf16 and of one shape")
         xs[:M].copy_(x, non_blocking=True)
         ls[:M].copy_(logits, non_blocking=True)
         if M < mb:

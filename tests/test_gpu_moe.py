@@ -421,6 +421,21 @@ def test_layer_class_refuses_what_does_not_fit():
     assert layer(torch.zeros((0, 256), device="cuda").bfloat16(), torch.zeros((0, 8), device="cuda")).shape == (0, 256)
 
 
+def test_layer_class_graphs_take_what_direct_calls_take():
+    layer, _, _ = _layer()
+    layer.capture(buckets=(4,))
+    g = _gen(6)
+    x, lg = torch.randn((4, 256), generator=g).bfloat16().cuda(), torch.randn((4, 8), generator=g).cuda()
+    for call in (layer, layer.layer):
+        for bad in ((x[:, :1], lg, None), (x, lg[:1], None), (x, lg[:, :1], None), (x.float(), lg, None),
+                    (x, lg, x[:1]), (x, lg, x.float())):
+            with pytest.raises(ValueError):
+                call(*bad)
+    # logits of another type than the graph's keep their own values
+    y = layer(x, lg.bfloat16())
+    assert torch.equal(y.view(torch.int16), layer.layer(x, lg.bfloat16()).view(torch.int16))
+
+
 def test_two_graphs_and_two_streams_at_once():
     # each call brings its own workspace: graphs captured separately may run side by side
     layer, _, _ = _layer(E=16, H=512, I=208, k=4)
