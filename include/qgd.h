@@ -331,7 +331,9 @@ QGD_API qgd_status qlinear_nvfp4_bf16(const void* x_bf16, int ldx, const void* w
  * reads device data on the host: a run of them can be captured into a CUDA
  * graph and replayed with other routings.  Workspaces of these calls need no
  * zero-filling, hold nothing between calls, and must not be shared by calls
- * that may overlap.  All results are deterministic.
+ * that may overlap.  Their first 64 KiB, the counter header of the dense
+ * calls, are neither read nor written: a workspace of those can serve these
+ * calls too and still holds its zeros.  All results are deterministic.
  * ------------------------------------------------------------------- */
 typedef enum { QGD_DTYPE_BF16 = 0, QGD_DTYPE_FP32 = 1 } qgd_dtype;
 typedef enum { QGD_SCORE_SOFTMAX = 0, QGD_SCORE_SIGMOID = 1 } qgd_score;

@@ -731,14 +731,17 @@ qgd_status run_layer(int fmt, const void* x_bf16, int ldx, const void* wq, const
 
 // ---------------------------------------------------------------------------
 // Grouped GEMM over experts: plan and workspace (arrival counters, codes,
-// scales, partials of tiles shared by several CTAs).
+// scales, partials of tiles shared by several CTAs).  All of it lies behind the
+// counter header of the dense calls, so that a workspace can serve those too:
+// these counters are cleared at the start of a call and left as they end, where
+// the header's have to stay zero between calls.
 // ---------------------------------------------------------------------------
 constexpr int kMaxExpertCtas = 256;  // SMs of any sm_100 part
 
 struct ExpertPlan {
   int tok = 0, n_tiles = 0, ctas = 0;
   bool code_once = false;  // code each row of x once and copy the codes into sorted order
-  size_t q_off = 0, s_off = 0, part_off = 0, q0_off = 0, s0_off = 0, total = 0;
+  size_t ticket_off = 0, q_off = 0, s_off = 0, part_off = 0, q0_off = 0, s0_off = 0, total = 0;
 };
 
 // x_rows: rows of x behind an order, or 0 without one
@@ -751,7 +754,8 @@ ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
   p.tok = per_expert < 44 ? 64 : per_expert < 112 ? 128 : 256;
   p.n_tiles = act ? (N + 63) / 64 : (N + 127) / 128;
   p.ctas = g_num_sms < kMaxExpertCtas ? g_num_sms : kMaxExpertCtas;
-  p.q_off = align256(static_cast<size_t>(p.ctas) * 4);
+  p.ticket_off = kTicketBytes;
+  p.q_off = align256(p.ticket_off + static_cast<size_t>(p.ctas) * 4);
   p.s_off = align256(p.q_off + static_cast<size_t>(rows) * K);
   p.part_off = align256(p.s_off + static_cast<size_t>(rows) * 4);
   p.total = p.part_off + (p.tok <= 128 ? static_cast<size_t>(p.ctas) * 2 * p.tok * kSwapTileN * 4 : 0);
@@ -1098,7 +1102,8 @@ qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl
 
 size_t qgd_moe_sort_workspace_size(int pairs, int E) {
   if (pairs <= 0 || E <= 0 || E > kMaxExperts) return 0;
-  return align256(sort_workspace(pairs, E));
+  const size_t counts = sort_workspace(pairs, E);  // behind the dense calls' counter header
+  return counts ? kTicketBytes + align256(counts) : 0;
 }
 
 qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws, size_t ws_bytes,
@@ -1113,8 +1118,8 @@ qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, 
     return fail(QGD_ERR_WORKSPACE, "sort workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : 0);
   qgd_status st = check_device();
   if (st != QGD_OK) return st;
-  const cudaError_t e = launch_sort(ids, pairs, E, offsets, order, pos, static_cast<int*>(ws),
-                                    static_cast<cudaStream_t>(stream));
+  int* counts = need > 0 ? reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kTicketBytes) : nullptr;
+  const cudaError_t e = launch_sort(ids, pairs, E, offsets, order, pos, counts, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QGD_OK : cuda_fail(e, "moe_sort launch");
 }
 
@@ -1172,7 +1177,7 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   a.sw = sw;
   a.y = static_cast<uint16_t*>(y_bf16);
   a.partial = reinterpret_cast<uint32_t*>(wsb + p.part_off);
-  a.tickets = reinterpret_cast<unsigned*>(wsb);
+  a.tickets = reinterpret_cast<unsigned*>(wsb + p.ticket_off);
   a.E = E;
   a.P = rows;
   a.N = N;

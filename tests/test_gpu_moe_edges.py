@@ -1,0 +1,66 @@
+"""Mixture-of-experts calls on the GPU at the edges of what they take: shared
+workspaces, extreme values, other streams, refusals."""
+import pytest
+import torch
+
+import moelib
+import quantized_gemm_decode_b200 as qgd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    qgd.lib()
+    yield
+    for f in (qgd.FMT_FP8_DYNAMIC, qgd.FMT_W8A8_INT8):
+        qgd.qgd_set_override(f)
+    torch.cuda.synchronize()
+    assert qgd.qgd_device_error() == 0
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _bits(t):
+    return t.view(torch.int16)
+
+
+def _weights(E, rows, K, int8, seed):
+    g = _gen(seed)
+    if int8:
+        wq = torch.randint(-127, 128, (E, rows, K), generator=g, dtype=torch.int8)
+    else:
+        wq = (100 * torch.randn((E, rows, K), generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return wq, 2e-4 * (0.5 + torch.rand((E, rows), generator=g))
+
+
+# ---------------------------------------------------------------------------
+# one workspace for expert calls and dense calls
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+@pytest.mark.parametrize("reduce", [qgd.REDUCE_LAST_CTA, qgd.REDUCE_TWO_PASS])
+def test_a_workspace_serves_expert_and_dense_calls(fmt, reduce):
+    int8 = fmt == "w8a8_int8"
+    fid = qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC
+    E, K, N, M = 6, 1024, 512, 4
+    wq, sw = (t.cuda() for t in _weights(E, N, K, int8, 1))
+    x = torch.randn((M, K), generator=_gen(2)).bfloat16().cuda()
+    qgd.qgd_set_override(fid, qgd.VARIANT_SWAP_AB, 4, reduce, 0, 0, qgd.SCHEDULE_GRID)
+    assert qgd.qgd_workspace_size(fid, M, N, K) > 0  # the dense plan counts arrivals in its workspace
+    ref = qgd.qlinear_bf16(fid, x, wq[0], sw[0], ws=qgd.Workspace(1 << 23)).clone()
+    shared = qgd.Workspace(1 << 23)
+    for T, k in ((3, 2), (700, 3), (5000, 2)):  # split tiles, pair tiles, several blocks of pairs
+        ids = torch.randint(0, E, (T, k), generator=_gen(T), dtype=torch.int32).cuda()
+        xe = torch.randn((T, K), generator=_gen(T)).bfloat16().cuda()
+        own = qgd.moe_sort(ids, E)
+        off, order, pos = qgd.moe_sort(ids, E, ws=shared)
+        for a, b in zip(own, (off, order, pos)):
+            assert torch.equal(a, b)
+        y = qgd.qlinear_experts_bf16(fid, xe, wq, sw, off, order=order, top_k=k, ws=shared)
+        assert not shared.buf[:64 * 1024].any()
+        dense = qgd.qlinear_bf16(fid, x, wq[0], sw[0], ws=shared)
+        again = qgd.qlinear_experts_bf16(fid, xe, wq, sw, off, order=order, top_k=k, ws=shared)
+        assert torch.equal(_bits(dense), _bits(ref))
+        assert torch.equal(_bits(y), _bits(again))

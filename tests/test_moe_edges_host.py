@@ -1,0 +1,24 @@
+"""CPU checks of the mixture-of-experts calls at the edges of what they take."""
+import pytest
+import torch
+
+import quantized_gemm_decode_b200 as qgd
+from quantized_gemm_decode_b200 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+    qgd.lib()
+
+
+HEADER = 64 * 1024  # the dense calls' arrival counters, zero between calls
+
+
+def test_workspaces_leave_room_for_the_dense_calls_counters():
+    # two blocks of pairs, 8 experts: 2 x 8 counts
+    assert qgd.qgd_moe_sort_workspace_size(4096, 8) >= HEADER + 2 * 8 * 4
+    assert qgd.qgd_moe_sort_workspace_size(2048, 8) == 0  # one block needs none
+    for fmt in (qgd.FMT_W8A8_INT8, qgd.FMT_FP8_DYNAMIC):
+        # codes and scales of one row, and an arrival counter per SM
+        assert qgd.qgd_experts_workspace_size(fmt, 1, 1, 4, 64, 256) >= HEADER + 148 * 4 + 256 + 4
