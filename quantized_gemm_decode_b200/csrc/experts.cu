@@ -367,10 +367,16 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
   else tma_load_2d(dst, map, bar, x, y, policy);
 }
 
-// The fast exponential's and quotient's errors (2^-20 together) are far below
-// bf16's half step.  The exponent is held below 80, where the fast quotient's
-// divisor is still in range and silu(g) is below every bf16 result's concern.
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(fminf(-g, 80.f))); }
+// g / (1 + exp(-g)).  The fast exponential is within (2 + 1.2 |g|) 2^-23, relative,
+// and the quotient within 2^-22: far below bf16's half step.  exp(-g) leaves fp32's
+// range at -88.7, and the fast quotient gives 0 for divisors above 2^126; below -80
+// the divisor is exp(-g) to the last bit, so the result is g * exp(g), which goes
+// down to fp32's last subnormal (an infinite gate gives 0 * inf = NaN, as the formula does).
+__device__ __forceinline__ float silu(float g) {
+  const bool low = g < -80.f;
+  const float e = __expf(low ? g : -g);
+  return low ? g * e : __fdividef(g, 1.f + e);
+}
 
 template <int kFmt>
 __device__ __forceinline__ float acc_value(uint32_t bits) {

@@ -64,3 +64,52 @@ def test_a_workspace_serves_expert_and_dense_calls(fmt, reduce):
         again = qgd.qlinear_experts_bf16(fid, xe, wq, sw, off, order=order, top_k=k, ws=shared)
         assert torch.equal(_bits(dense), _bits(ref))
         assert torch.equal(_bits(y), _bits(again))
+
+
+# ---------------------------------------------------------------------------
+# the gated activation over fp32's range
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+@pytest.mark.parametrize("rows", [1, 60, 300])
+def test_gates_far_below_zero(fmt, rows):
+    # One live input per row, whose code is the largest (scale 1), times weights of 1: the
+    # products are qmax * sw, so the scales place gates and ups anywhere.
+    int8 = fmt == "w8a8_int8"
+    qmax = 127.0 if int8 else 448.0
+    gates = [0.0, -1.0, 5.0, 60.0, -60.0, -79.5, -80.5, -86.0, -88.5, -89.0, -95.0, -100.0, -103.0, -120.0, -1e20, -1e36]
+    ups = [1.0, -3.0, 1e10, 1e30]
+    N, K = len(gates) * len(ups), 16
+    g = torch.tensor(gates).repeat(len(ups)) / qmax
+    u = torch.tensor(ups).repeat_interleave(len(gates)) / qmax
+    sw = torch.cat([g, u])[None]
+    wq = torch.zeros((1, 2 * N, K), dtype=torch.int8 if int8 else torch.uint8)
+    wq[:, :, 0] = 1 if int8 else 0x38  # e4m3 1.0
+    x = torch.zeros((rows, K), dtype=torch.bfloat16)
+    x[:, 0] = qmax
+    off = torch.tensor([0, rows], dtype=torch.int32)
+    y = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC, x.cuda(), wq.cuda(), sw.cuda(),
+                                 off.cuda(), act=qgd.ACT_SILU_MUL)
+    ref, mag = moelib.experts(x, wq, sw, off, None, 1, True, int8)
+    # Half a bf16 step; up to g = -104 the exponential's (2 + 1.2 * 104) 2^-23 and the gate's two
+    # roundings, 2^-23 together, times |g|: 2^-14 in all; the subnormal exponential's step times
+    # |g u|; and half of bf16's smallest step.
+    size_g, size_u = mag[:, :N], mag[:, N:]
+    tol = abs(ref) * (2.0 ** -8 + 2.0 ** -14) + 2.0 ** -149 * (size_g.clip(max=110.0) + 2) * size_u + 2.0 ** -133
+    moelib.close(y, ref, tol, fmt)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_infinite_gates(rows):
+    # inf / (1 + 0) = inf, and -inf / (1 + inf) = NaN
+    N, K, inf = 16, 16, float("inf")
+    sw = torch.ones((1, 2 * N))
+    sw[0, :4] = torch.tensor([inf, -inf, 1.0, float("nan")])
+    wq = torch.zeros((1, 2 * N, K), dtype=torch.int8)
+    wq[:, :, 0] = 1
+    x = torch.zeros((rows, K), dtype=torch.bfloat16)
+    x[:, 0] = 127.0
+    off = torch.tensor([0, rows], dtype=torch.int32)
+    y = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, x.cuda(), wq.cuda(), sw.cuda(), off.cuda(),
+                                 act=qgd.ACT_SILU_MUL).float().cpu()
+    assert (y[:, 0] == inf).all() and y[:, 1].isnan().all() and y[:, 3].isnan().all()
+    assert (y[:, 2] == 16128.0).all()  # 127 * 127 in bf16
