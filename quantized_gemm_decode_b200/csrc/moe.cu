@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kVPT <= 8 ? 8 : 1) route_ker
       if (x[j] > -INFINITY) {
         const double d = static_cast<double>(x[j]) - static_cast<double>(mx);
         const float r = static_cast<float>(d);
-        total += static_cast<double>(expf(r)) * (1.0 + (d - static_cast<double>(r)));
+        const float ex = expf(r);
+        // (d may lie below fp32's range, a masked logit under an infinite one: r and d - r are infinite there)
+        if (ex > 0.f) total += static_cast<double>(ex) * (1.0 + (d - static_cast<double>(r)));
       }
     }
 #pragma unroll

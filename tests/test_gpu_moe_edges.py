@@ -113,3 +113,28 @@ def test_infinite_gates(rows):
                                  act=qgd.ACT_SILU_MUL).float().cpu()
     assert (y[:, 0] == inf).all() and y[:, 1].isnan().all() and y[:, 3].isnan().all()
     assert (y[:, 2] == 16128.0).all()  # 127 * 127 in bf16
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_infinite_logits_over_masked_ones(dtype, score, renormalize, bias):
+    # differences of logits outside fp32's range, with experts left over at finite logits
+    inf, low, E = float("inf"), torch.finfo(dtype).min, 64
+    rows = [[inf, inf, low, 0.0], [inf, low, low, low], [1e38, 1e38, -3e38, -1e38], [low] * 4, [0.0, low, low, -inf],
+            [inf, inf, -inf, low], [3e38, 3e38, 3e38, -3e38]]
+    logits = torch.full((len(rows), E), low)
+    for t, r in enumerate(rows):
+        logits[t, 5:9] = torch.tensor(r)
+    logits[-1, 40:] = -inf
+    logits = logits.to(dtype)
+    b = torch.linspace(-0.25, 0.25, E) if bias else None
+    w, ids = qgd.moe_route(logits.cuda(), 4, score=score, renormalize=renormalize, bias=None if b is None else b.cuda())
+    rw, ri = moelib.route(logits, 4, score=score, renormalize=renormalize, bias=b)
+    assert (ids.cpu().numpy() == ri).all()
+    # one rounding to fp32 of a value computed to a few fp32 steps (2^-20 together)
+    moelib.close(w, rw, abs(rw) * 2.0 ** -20 + 2.0 ** -140)
