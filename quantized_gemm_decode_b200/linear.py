@@ -130,9 +130,9 @@ class QuantizedExperts:
     A call up to GRAPH_MAX_M tokens replays the graph of its bucket once
     capture() has run (rows behind the call's tokens are padding, routed to no
     expert); other calls, and those with logits of another type than the
-    graph's, launch directly.  Direct calls may overlap (other
-    streams); a captured bucket's buffers are shared by its replays, which
-    must not."""
+    graph's, launch directly.  Every call returns a tensor of its own.  Direct
+    calls may overlap (other streams); a captured bucket's buffers are shared
+    by its replays, which must not."""
 
     def __init__(self, w_gate_up, w_down, top_k: int, fmt: str = "w8a8_int8", route: dict | None = None,
                  weights: tuple | None = None):
@@ -208,7 +208,7 @@ class QuantizedExperts:
         else:
             adds[:M].copy_(add, non_blocking=True)
         g.replay()
-        return ys[:M]
+        return ys[:M].clone()
 
 
 class DecodeStep:

@@ -138,3 +138,32 @@ def test_route_infinite_logits_over_masked_ones(dtype, score, renormalize, bias)
     assert (ids.cpu().numpy() == ri).all()
     # one rounding to fp32 of a value computed to a few fp32 steps (2^-20 together)
     moelib.close(w, rw, abs(rw) * 2.0 ** -20 + 2.0 ** -140)
+
+
+# ---------------------------------------------------------------------------
+# the layer class
+# ---------------------------------------------------------------------------
+def _layer(E=8, H=256, I=96, k=3, fmt="w8a8_int8", **route):
+    from quantized_gemm_decode_b200.linear import QuantizedExperts
+    g = _gen(E + H)
+    gu = (0.05 * torch.randn((E, 2 * I, H), generator=g)).bfloat16().cuda()
+    dn = (0.05 * torch.randn((E, H, I), generator=g)).bfloat16().cuda()
+    return QuantizedExperts(gu, dn, k, fmt, route=route)
+
+
+def _inputs(M, seed, H=256, E=8):
+    g = _gen(seed)
+    return torch.randn((M, H), generator=g).bfloat16().cuda(), torch.randn((M, E), generator=g).cuda()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_results_of_earlier_calls_stay_as_they_were(captured):
+    layer = _layer()
+    if captured:
+        layer.capture(buckets=(1, 4))
+    ins = [_inputs(M, 30 + i) for i, M in enumerate((4, 4, 3, 1, 1))]
+    got = [layer(x, lg) for x, lg in ins]
+    for (x, lg), y in zip(ins, got):
+        assert torch.equal(_bits(y), _bits(layer.layer(x, lg)))
+    got[0].zero_()  # and are the caller's to write
+    assert torch.equal(_bits(layer(*ins[1])), _bits(got[1]))
