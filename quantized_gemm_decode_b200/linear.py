@@ -199,6 +199,9 @@ class QuantizedExperts:
         self._check(x, logits)
         if x.dtype != torch.bfloat16 or (add is not None and (add.dtype != torch.bfloat16 or add.shape != x.shape)):
             raise ValueError("x and add must be bf16 and of one shape")
+        for t, name in ((x, "x"), (logits, "logits"), (add, "add")):
+            if t is not None and t.device != xs.device:
+                raise ValueError(f"{name} is on {t.device}, expected {xs.device}")
         xs[:M].copy_(x, non_blocking=True)
         ls[:M].copy_(logits, non_blocking=True)
         if M < mb:

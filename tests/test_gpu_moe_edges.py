@@ -167,3 +167,15 @@ def test_results_of_earlier_calls_stay_as_they_were(captured):
         assert torch.equal(_bits(y), _bits(layer.layer(x, lg)))
     got[0].zero_()  # and are the caller's to write
     assert torch.equal(_bits(layer(*ins[1])), _bits(got[1]))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_operands_on_the_host_are_refused(captured):
+    layer = _layer()
+    if captured:
+        layer.capture(buckets=(4,))
+    x, lg = _inputs(4, 3)
+    for bad in ((x.cpu(), lg, None), (x, lg.cpu(), None), (x, lg, x.cpu()), (x.cpu().pin_memory(), lg, None)):
+        with pytest.raises(ValueError, match="cuda|CUDA"):
+            layer(*bad)
+    assert layer(x, lg, add=x).shape == (4, 256)
