@@ -153,7 +153,8 @@ class QuantizedExperts:
     def _quantize(self, w: torch.Tensor) -> tuple:
         E, rows, K = w.shape
         qt = qgd.QTYPE_INT8 if self.fmt == "w8a8_int8" else qgd.QTYPE_E4M3
-        wq, sw = qgd.quant_weight_per_channel(w.reshape(E * rows, K), qt)
+        with torch.cuda.device(w.device):  # (the quantizer launches on the current device)
+            wq, sw = qgd.quant_weight_per_channel(w.reshape(E * rows, K), qt)
         return wq.view(E, rows, K), sw.view(E, rows)
 
     def _check(self, x, logits) -> None:

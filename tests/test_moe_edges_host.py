@@ -22,3 +22,31 @@ def test_workspaces_leave_room_for_the_dense_calls_counters():
     for fmt in (qgd.FMT_W8A8_INT8, qgd.FMT_FP8_DYNAMIC):
         # codes and scales of one row, and an arrival counter per SM
         assert qgd.qgd_experts_workspace_size(fmt, 1, 1, 4, 64, 256) >= HEADER + 148 * 4 + 256 + 4
+
+
+def test_layer_quantizes_its_weights_on_their_own_device(monkeypatch):
+    # the quantizer launches on the current device, which need not be the weights'
+    from quantized_gemm_decode_b200.linear import QuantizedExperts
+    current = ["the caller's"]
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    seen = []
+
+    def quantizer(w, qtype):
+        seen.append((current[-1], w.device))
+        return torch.zeros(w.shape, dtype=torch.int8), torch.ones(w.shape[0])
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(qgd, "quant_weight_per_channel", quantizer)
+    layer = QuantizedExperts(torch.zeros((2, 32, 64)), torch.zeros((2, 64, 16)), 1)
+    assert layer.gate_up.shape == (2, 32, 64) and layer.down_s.shape == (2, 64)
+    assert len(seen) == 2 and all(cur == dev for cur, dev in seen)
