@@ -185,7 +185,9 @@ class QuantizedExperts:
                 self.layer(x, logits, add=add, y=y)  # warm-up outside capture
             torch.cuda.current_stream(self.device).wait_stream(s)
             g = torch.cuda.CUDAGraph()
-            with torch.cuda.device(self.device), torch.cuda.graph(g):
+            # (on a stream of this device: the default capture stream is one of the device that was
+            # current when the process first captured)
+            with torch.cuda.device(self.device), torch.cuda.graph(g, stream=s):
                 self.layer(x, logits, add=add, y=y)
             self._graphs[mb] = (g, x, logits, add, y)
 

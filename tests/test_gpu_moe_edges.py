@@ -179,3 +179,17 @@ def test_operands_on_the_host_are_refused(captured):
         with pytest.raises(ValueError, match="cuda|CUDA"):
             layer(*bad)
     assert layer(x, lg, add=x).shape == (4, 256)
+
+
+def test_graphs_are_captured_on_a_stream_of_the_layers_device(monkeypatch):
+    layer, streams, graph = _layer(), [], torch.cuda.graph
+
+    def recording(g, pool=None, stream=None, **kw):
+        streams.append(stream)
+        return graph(g, pool=pool, stream=stream, **kw)
+
+    monkeypatch.setattr(torch.cuda, "graph", recording)
+    layer.capture(buckets=(1, 4))
+    assert len(streams) == 2 and all(s is not None and s.device == layer.device for s in streams)
+    x, lg = _inputs(3, 4)
+    assert torch.equal(_bits(layer(x, lg)), _bits(layer.layer(x, lg)))
