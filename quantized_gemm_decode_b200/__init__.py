@@ -711,7 +711,8 @@ def _on(device: int, stream) -> contextlib.ExitStack:
     stack.enter_context(torch.cuda.device(device))
     if stream is not None:
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            # (address 0 is the default stream; ExternalStream would make a new one of it)
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
         if stream.device.index != device:
             stack.close()
             raise ValueError(f"stream is on {stream.device}, the operands on cuda:{device}")

@@ -193,3 +193,24 @@ def test_graphs_are_captured_on_a_stream_of_the_layers_device(monkeypatch):
     assert len(streams) == 2 and all(s is not None and s.device == layer.device for s in streams)
     x, lg = _inputs(3, 4)
     assert torch.equal(_bits(layer(x, lg)), _bits(layer.layer(x, lg)))
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+def test_streams_given_by_address():
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.default_stream(), side):
+        for other in (torch.cuda.default_stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(other), qgd._on(0, stream.cuda_stream):
+                assert torch.cuda.current_stream().cuda_stream == stream.cuda_stream
+    # on the default stream, a call by its address follows the work queued there
+    ids = torch.randint(0, 16, (4000, 4), generator=_gen(1), dtype=torch.int32).cuda()
+    ref = [t.clone() for t in qgd.moe_sort(ids, 16)]
+    for _ in range(10):
+        late = torch.zeros_like(ids)
+        torch.cuda._sleep(2_000_000)
+        late.copy_(ids)
+        got = qgd.moe_sort(late, 16, stream=torch.cuda.default_stream().cuda_stream)
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
