@@ -750,6 +750,13 @@ def _operand(t, name: str, dtypes, shape, device: int, contiguous: bool = True) 
     raise ValueError(f"{name} must be contiguous")
 
 
+def _below_2_31(n: int, what: str) -> None:
+    """n: sizes or'ed together.  The library takes them in 32 bits, and ctypes cuts
+    off what is above."""
+    if n >> 31:
+        raise ValueError(f"{what}: sizes and strides must be below 2**31")
+
+
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor with unit column stride (dense, or a column
     slice of a wider matrix)."""
@@ -761,6 +768,7 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
         return cols
     if row < cols:
         raise ValueError(f"{name} must have a row stride of at least its {cols} columns")
+    _below_2_31(row, name)
     return row
 
 
@@ -784,6 +792,7 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 
 @functools.lru_cache(maxsize=256)
 def _route_desc(top_k, score, groups, topk_groups, group_top, renormalize, scale):
+    _below_2_31(abs(top_k) | abs(groups) | abs(topk_groups) | abs(group_top), "top_k, groups")
     return ctypes.byref(_Route(top_k, score, groups, topk_groups, group_top, renormalize, scale))
 
 
@@ -811,7 +820,10 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     T, E = logits.shape
+    _below_2_31(T | E, "logits")
+    desc = _route_desc(top_k, _SCORES[score], groups, topk_groups, group_top, 1 if renormalize else 0, scale)
     x = _operand(logits, "logits", _LOGITS, None, dev, False)
+    ldl = _row_stride(logits, "logits")
     b = None if bias is None else _operand(bias, "bias", _F32, (E,), dev)
     out = (T, top_k if top_k > 0 else 0)
     if weights is None:
@@ -824,10 +836,8 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
         ip = ids.data_ptr()
     else:
         ip = _operand(ids, "ids", _I32, out, dev)
-    st = (_lib or lib()).moe_route(x, 0 if logits.dtype is torch.bfloat16 else 1, T, E, _row_stride(logits, "logits"),
-                                   b, _route_desc(top_k, _SCORES[score], groups, topk_groups, group_top,
-                                                  1 if renormalize else 0, scale),
-                                   wp, ip, _raw_stream(dev))
+    st = (_lib or lib()).moe_route(x, 0 if logits.dtype is torch.bfloat16 else 1, T, E, ldl, b, desc, wp, ip,
+                                   _raw_stream(dev))
     if st:
         _check(st, "moe_route")
     return weights, ids
@@ -855,6 +865,7 @@ def moe_sort(ids: torch.Tensor, num_experts: int, offsets=None, order=None, pos=
             return moe_sort(ids, num_experts, offsets, order, pos, ws)
     at = _operand(ids, "ids", _I32, None, dev)
     P = ids.numel()
+    _below_2_31(P | abs(num_experts), "ids, num_experts")
     n_off = num_experts + 1 if num_experts > 0 else 1
     if offsets is None:
         offsets = _new(torch.int32, n_off)
@@ -921,13 +932,15 @@ def qlinear_experts_bf16(fmt: int, x: torch.Tensor, wq, sw, offsets, order=None,
     if order is not None:
         op = _operand(order, "order", _I32, None, dev)
         rows = order.numel()
+    _below_2_31(x_rows | K | E | n_all | rows | abs(top_k) | abs(fmt), "x, wq, order, top_k")
+    ldx = _row_stride(x, "x")
     if y is None:
         y = _new(torch.bfloat16, rows, N)
         yp = y.data_ptr()
     else:
         yp = _operand(y, "y", _BF16, (rows, N), dev)
     wsp, wsn, _keep = _scratch(ws, _experts_need(dev, fmt, rows, 0 if op is None else x_rows, E, N, K, act), x)
-    st = (_lib or lib()).qlinear_experts_bf16(fmt, xp, _row_stride(x, "x"), x_rows, op, top_k,
+    st = (_lib or lib()).qlinear_experts_bf16(fmt, xp, ldx, x_rows, op, top_k,
                                               _operand(offsets, "offsets", _I32, (E + 1,), dev), E, rows, wp,
                                               _operand(sw, "sw", _F32, (E, n_all), dev), yp, N, K, act, wsp, wsn,
                                               _raw_stream(dev))
@@ -951,6 +964,7 @@ def moe_combine(h: torch.Tensor, pos, weights, add=None, y=None, stream=None):
         raise ValueError("h must be [rows, H] and pos [tokens, top_k]")
     rows, H = h.shape
     T, k = pos.shape
+    _below_2_31(rows | H | T | k, "h, pos")
     ap, lda = None, 0
     if add is not None:
         ap, lda = _operand(add, "add", _BF16, (T, H), dev, contiguous=False), _row_stride(add, "add")

@@ -214,3 +214,27 @@ def test_streams_given_by_address():
         got = qgd.moe_sort(late, 16, stream=torch.cuda.default_stream().cuda_stream)
         for a, b in zip(got, ref):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def test_sizes_and_strides_past_32_bits_are_refused():
+    # (nothing of the buffer is written or read)
+    n = (1 << 32) + 64
+    buf = torch.empty(n, dtype=torch.int32, device="cuda")
+    wide = buf.view(torch.bfloat16)
+    far = wide.as_strided((2, 64), (n, 1))
+    wq, sw = (t.cuda() for t in _weights(2, 32, 64, True, 1))
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    h, one = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda"), torch.ones((2, 1), device="cuda")
+    pos = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    for call in (lambda: qgd.moe_route(far, 2), lambda: qgd.moe_route(wide[:n, None], 1),
+                 lambda: qgd.moe_route(h, (1 << 32) + 1),
+                 lambda: qgd.moe_sort(buf, 8), lambda: qgd.moe_sort(pos, (1 << 32) + 8),
+                 lambda: qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, far, wq, sw, off),
+                 lambda: qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, h, wq, sw, off, order=buf),
+                 lambda: qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, h, wq, sw, off, order=pos.view(-1), top_k=1 << 32),
+                 lambda: qgd.moe_combine(h, pos, one, add=far)):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            call()

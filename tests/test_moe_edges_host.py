@@ -50,3 +50,18 @@ def test_layer_quantizes_its_weights_on_their_own_device(monkeypatch):
     layer = QuantizedExperts(torch.zeros((2, 32, 64)), torch.zeros((2, 64, 16)), 1)
     assert layer.gate_up.shape == (2, 32, 64) and layer.down_s.shape == (2, 64)
     assert len(seen) == 2 and all(cur == dev for cur, dev in seen)
+
+
+def test_sizes_and_strides_past_32_bits_are_refused():
+    # (the library takes ints: a stride of 2**32 + 64 would arrive as 64)
+    for stride in (1 << 31, (1 << 32) + 64):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qgd._row_stride(torch.empty_strided((2, 64), (stride, 1), device="meta"), "x")
+    assert qgd._row_stride(torch.empty_strided((2, 64), ((1 << 31) - 8, 1), device="meta"), "x") == (1 << 31) - 8
+    assert qgd._row_stride(torch.empty_strided((1, 64), (1 << 40, 1), device="meta"), "x") == 64  # one row: unused
+    for n in (1 << 31, (1 << 32) + 2, 1 << 40):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qgd._below_2_31(n | 5, "x")
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qgd._route_desc(n, 0, 1, 1, 1, 1, 1.0)
+    qgd._below_2_31((1 << 31) - 1, "x")
