@@ -400,8 +400,8 @@ QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int*
  * Offsets are read on the device, clamped to [0, rows]; a source row outside
  * [0, x_rows) counts as zeros.  N % 16 == 0; K % 16 == 0, K <= 16384;
  * 1 <= E <= QGD_MAX_EXPERTS; (rows / 64 + E) * N / 64 * K / 256 and
- * (rows / 64 + 1) * E below 2^31 and the weight rows of all experts below 2^30
- * (else QGD_ERR_UNSUPPORTED).  x, wq, y and ws 16-byte aligned.  y must not
+ * (rows / 64 + 1) * E below 2^31, rows and the weight rows of all experts below
+ * 2^30 (else QGD_ERR_UNSUPPORTED).  x, wq, y and ws 16-byte aligned.  y must not
  * overlap the inputs.  Workspace: qgd_experts_workspace_size() bytes, its
  * x_rows 0 for a call without an order. */
 QGD_API size_t qgd_experts_workspace_size(int fmt, int rows, int x_rows, int E, int N, int K, int act);

@@ -1148,10 +1148,11 @@ qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, int x_rows
   if (order && top_k < 1) return fail(QGD_ERR_INVALID, "top_k=%d must be positive", top_k);
   if (!order && rows > x_rows) return fail(QGD_ERR_INVALID, "%d rows of %d without an order", rows, x_rows);
   const long long n_all = static_cast<long long>(N) * (act == QGD_ACT_SILU_MUL ? 2 : 1);
-  // (the kernel counts tiles, and tiles x K steps, in 32 bits; its running tile
-  // counts stay there whatever the offsets hold)
+  // (the kernel counts rows, tiles, and tiles x K steps in 32 bits, an expert's rows
+  // plus its token tiles among them; its running tile counts stay there whatever the
+  // offsets hold)
   const long long token_tiles = rows / 64;
-  if (n_all * E >= (1LL << 30) || (token_tiles + E) * ((N + 63) / 64) * ((K + 255) / 256) >= (1LL << 31) ||
+  if (rows >= (1 << 30) || n_all * E >= (1LL << 30) || (token_tiles + E) * ((N + 63) / 64) * ((K + 255) / 256) >= (1LL << 31) ||
       (token_tiles + 1) * E >= (1LL << 31))
     return fail(QGD_ERR_UNSUPPORTED, "too many weight rows or tiles (rows=%d E=%d N=%d)", rows, E, N);
   if (rows == 0) return QGD_OK;

@@ -65,3 +65,13 @@ def test_sizes_and_strides_past_32_bits_are_refused():
         with pytest.raises(ValueError, match="2\\*\\*31"):
             qgd._route_desc(n, 0, 1, 1, 1, 1, 1.0)
     qgd._below_2_31((1 << 31) - 1, "x")
+
+
+@pytest.mark.parametrize("rows,unsupported", [((1 << 31) - 1, True), ((1 << 31) - (1 << 20), True), (1 << 30, True),
+                                              ((1 << 30) - 1, False)])
+@pytest.mark.parametrize("act", [0, 1])
+def test_rows_whose_tiles_would_pass_32_bits_are_refused(rows, unsupported, act):
+    # 2**31 - 2**20 rows of one expert: rows + token tiles wrap, and tiles would start at negative rows
+    at = 1 << 20  # an aligned address; without a workspace nothing is launched with it
+    st = qgd.lib().qlinear_experts_bf16(1, at, 16, 8, at, 2, at, 1, rows, at, at, at, 16, 16, act, None, 0, None)
+    assert st != 0 and (st == -2) == unsupported
