@@ -323,8 +323,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kVPT <= 8 ? 8 : 1) route_ker
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
+  const unsigned row = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);  // (the last block's may pass 2^31)
+  if (row >= static_cast<unsigned>(a.T)) return;
+  const int t = static_cast<int>(row);
   float x[kVPT], bias[kVPT];
   load_logits<kVPT, kBf16>(a, t, lane, x);
 #pragma unroll
@@ -711,7 +712,7 @@ cudaError_t launch_route_v(RouteArgs a, cudaStream_t st) {
     for (int l = 0; l <= 5; ++l)
       if (a.per == kVPT << l) a.span_log = l;
   a.vec_bias = whole && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  return launch_pdl(route_kernel<kVPT, kBf16>, static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps),
+  return launch_pdl(route_kernel<kVPT, kBf16>, (static_cast<unsigned>(a.T) + kRouteWarps - 1) / kRouteWarps,
                     kRouteWarps * 32, 0, st, a);
 }
 

@@ -238,3 +238,14 @@ def test_sizes_and_strides_past_32_bits_are_refused():
                  lambda: qgd.moe_combine(h, pos, one, add=far)):
         with pytest.raises(ValueError, match="2\\*\\*31"):
             call()
+
+
+def test_route_as_many_rows_as_an_int_counts():
+    # one expert, so every row's choice is known; 22 GB
+    T = (1 << 31) - 1
+    logits = torch.zeros((T, 1), dtype=torch.bfloat16, device="cuda")
+    logits[-1] = float("-inf")
+    w, ids = qgd.moe_route(logits, 1, score="sigmoid", renormalize=False)
+    assert w[-4:].flatten().tolist() == [0.5, 0.5, 0.5, 0.0] and ids[-4:].flatten().tolist() == [0, 0, 0, -1]
+    assert w[:2].flatten().tolist() == [0.5, 0.5]
+    assert int((ids[1 << 30:].view(-1) == 0).sum()) == T - (1 << 30) - 1
