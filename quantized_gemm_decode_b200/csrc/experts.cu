@@ -533,13 +533,16 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   griddep_wait();  // offsets, codes and scales come from the kernels before
   // token tiles of the experts before e, as a running sum in blocks of experts
   {
+    // (no expert's rows go past offsets[E], also where the offsets do not ascend: the
+    // quantizer has coded none behind it)
+    const int live = offset_of(a, a.E);
     int carry = 0;
     if (threadIdx.x == 0) pre[0] = 0;
     for (int e0 = 0; e0 < a.E; e0 += kThreads) {
       const int e = e0 + threadIdx.x;
       int v = 0;
       if (e < a.E) {
-        const int first = offset_of(a, e), cnt = offset_of(a, e + 1) - first;
+        const int first = min(offset_of(a, e), live), cnt = min(offset_of(a, e + 1), live) - first;
         off[e] = first;
         if (e == a.E - 1) off[a.E] = first + cnt;
         v = cnt > 0 ? (cnt + kTok - 1) / kTok : 0;
