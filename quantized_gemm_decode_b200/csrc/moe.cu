@@ -493,6 +493,14 @@ constexpr int kSortChunk = kSortThreads * kSortRounds;  // and pairs per block
 
 __host__ __device__ inline int count_stride(int E) { return (E + 3) & ~3; }  // a block's row of counts, whole vectors
 
+// Up to 64 K counts each block adds the others' up for itself: no launch in
+// between, but loads that grow with the square of the blocks.  Above, a kernel of
+// its own replaces the counts by their running sums, in time that grows with the
+// pairs.  By themselves / by the kernel, on B200: 262144 pairs over 256 experts (32 K
+// counts) 12.7 / 12.9 us, 524288 (64 K) 17.6 / 17.2, 2 M 133 / 56; 2 M over 16
+// (16 K) 24 / 43, 8 M (64 K) 163 / 163; 64 M over 1024, 780 ms / 2.6 ms.
+__host__ __device__ inline bool sums_apart(int blocks, int stride) { return blocks * stride > (1 << 16); }
+
 // Counts of each block's pairs per expert.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __restrict__ ids, int P, int E,
                                                                   int* __restrict__ counts) {
@@ -515,6 +523,29 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __r
   const int stride = count_stride(E);
   for (int e = threadIdx.x; e < stride; e += kSortThreads)
     counts[static_cast<size_t>(blockIdx.x) * stride + e] = e < E ? hist[e] : 0;
+}
+
+// Each block's counts become the counts of the blocks before it; the row behind
+// the last block's, the totals.  A thread per expert, 16 blocks' loads in flight.
+constexpr int kScanThreads = 64;
+
+__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(int* counts, int blocks, int stride) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int e = blockIdx.x * kScanThreads + threadIdx.x;
+  if (e >= stride) return;
+  int sum = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 16) {
+    int c[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i] = b0 + i < blocks ? counts[static_cast<size_t>(b0 + i) * stride + e] : 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (b0 + i < blocks) counts[static_cast<size_t>(b0 + i) * stride + e] = sum;
+      sum += c[i];
+    }
+  }
+  counts[static_cast<size_t>(blocks) * stride + e] = sum;
 }
 
 template <int kRounds>
@@ -541,7 +572,12 @@ __global__ void __launch_bounds__(kSortThreads)
     const int e = p < P ? __ldg(ids + p) : -1;
     id[r] = e >= 0 && e < E ? e : -1;
   }
-  if (!alone) {
+  if (sums_apart(gridDim.x, stride)) {
+    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+      before[e] = __ldg(counts + static_cast<size_t>(blockIdx.x) * stride + e);
+      total[e] = __ldg(counts + static_cast<size_t>(gridDim.x) * stride + e);
+    }
+  } else if (!alone) {
     // the blocks' counts, four experts a thread, the blocks dealt to as many threads as there are
     const int vecs = stride / 4, teams = kSortThreads / vecs;
     const int team = threadIdx.x / vecs, v = threadIdx.x - team * vecs;
@@ -737,7 +773,8 @@ int sort_blocks(int P) { return static_cast<int>((static_cast<long long>(P) + kS
 
 size_t sort_workspace(int P, int E) {
   const int blocks = sort_blocks(P);
-  return blocks > 1 ? static_cast<size_t>(blocks) * count_stride(E) * 4 : 0;
+  const int stride = count_stride(E);
+  return blocks > 1 ? static_cast<size_t>(blocks + (sums_apart(blocks, stride) ? 1 : 0)) * stride * 4 : 0;
 }
 
 template <int kRounds>
@@ -757,9 +794,15 @@ cudaError_t launch_sort(const int* ids, int P, int E, int* offsets, int* order, 
   if (P <= kSortThreads) return launch_place<1>(1, ids, P, E, offsets, order, pos, counts, stream);
   const unsigned blocks = static_cast<unsigned>(sort_blocks(P));
   if (blocks > 1) {
-    const cudaError_t e =
+    cudaError_t e =
         launch_pdl(sort_count_kernel, blocks, kSortThreads, static_cast<size_t>(E) * 4, stream, ids, P, E, counts);
     if (e != cudaSuccess) return e;
+    const int stride = count_stride(E);
+    if (sums_apart(static_cast<int>(blocks), stride)) {
+      e = launch_pdl(sort_scan_kernel, (stride + kScanThreads - 1) / kScanThreads, kScanThreads, 0, stream, counts,
+                     static_cast<int>(blocks), stride);
+      if (e != cudaSuccess) return e;
+    }
   }
   return launch_place<kSortRounds>(blocks, ids, P, E, offsets, order, pos, counts, stream);
 }

@@ -274,3 +274,46 @@ def test_offsets_that_descend_end_at_the_last(fmt, scale):
         first = int(cut[0])
         assert (y[:first] == 7.0).all()
         moelib.close(y[first:n], ref[first:n], tol[first:n])
+
+
+# ---------------------------------------------------------------------------
+# sort of many pairs
+# ---------------------------------------------------------------------------
+def _check_sort(ids, E):
+    off, order, pos = qgd.moe_sort(ids, E)
+    P = ids.numel()
+    live = (ids >= 0) & (ids < E)
+    ref = torch.sort(torch.where(live, ids, E), stable=True).indices
+    n = int(live.sum())
+    assert torch.equal(off[1:].long(), torch.bincount(ids[live].long(), minlength=E).cumsum(0)) and off[0] == 0
+    assert torch.equal(order[:n].long(), ref[:n]) and (order[n:] == -1).all()
+    want = torch.full((P,), -1, dtype=torch.int32, device="cuda")
+    want[ref[:n]] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(pos, want)
+
+
+# 2048 pairs a block; above 65536 counts the blocks' counts are summed by a kernel of their own
+@pytest.mark.parametrize("P,E", [(64 * 2048, 1024), (64 * 2048 + 1, 1024), (257 * 2048 - 1, 256), (8192 * 2048, 7),
+                                 (8192 * 2048 + 5, 7), (5_000_003, 33), (4_500_000, 1023), (9_000_001, 257)])
+def test_sort_of_many_pairs(P, E):
+    g = torch.Generator(device="cuda").manual_seed(P)
+    ids = torch.randint(0, E, (P,), generator=g, device="cuda", dtype=torch.int32)
+    ids[torch.rand(P, generator=g, device="cuda") < 0.1] = -1
+    _check_sort(ids, E)
+
+
+def test_sort_time_grows_with_the_pairs():
+    # (with every block adding up all blocks' counts, 64 M pairs took 780 ms, and 2 G would take minutes)
+    def ms(P):
+        ids = torch.zeros(P, dtype=torch.int32, device="cuda")
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            qgd.moe_sort(ids, 1024)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert ms(1 << 26) < 64 * ms(1 << 22)  # 16 times the pairs
