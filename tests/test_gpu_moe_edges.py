@@ -317,3 +317,87 @@ def test_sort_time_grows_with_the_pairs():
         return best
 
     assert ms(1 << 26) < 64 * ms(1 << 22)  # 16 times the pairs
+
+
+def _moe_args():
+    E, K, N = 4, 64, 32
+    wq, sw = (t.cuda() for t in _weights(E, N, K, True, 1))
+    f = dict(dtype=torch.float32, device="cuda")
+    i = dict(dtype=torch.int32, device="cuda")
+    return dict(logits=torch.zeros((6, 16), **f), ids=torch.zeros((6, 2), **i), wq=wq, sw=sw,
+                x=torch.zeros((6, K), dtype=torch.bfloat16, device="cuda"), offsets=torch.zeros(E + 1, **i),
+                order=torch.zeros(12, **i), h=torch.zeros((12, N), dtype=torch.bfloat16, device="cuda"),
+                pos=torch.zeros((6, 2), **i), weights=torch.zeros((6, 2), **f))
+
+
+def _call(name, a):
+    if name == "route":
+        return qgd.moe_route(a["logits"], 2, score=a.get("score", "softmax"), bias=a.get("bias"),
+                             weights=a.get("weights_out"), ids=a.get("ids_out"), stream=a.get("stream"))
+    if name == "sort":
+        return qgd.moe_sort(a["ids"], 4, offsets=a.get("offsets_out"), order=a.get("order_out"), pos=a.get("pos_out"))
+    if name == "experts":
+        return qgd.qlinear_experts_bf16(a.get("fmt", qgd.FMT_W8A8_INT8), a["x"], a["wq"], a["sw"], a["offsets"],
+                                        order=a["order"], top_k=2, act=a.get("act", qgd.ACT_NONE), y=a.get("y"),
+                                        ws=a.get("ws"))
+    return qgd.moe_combine(a["h"], a["pos"], a["weights"], add=a.get("add"), y=a.get("y"))
+
+
+@pytest.mark.parametrize("name", ["route", "sort", "experts", "combine"])
+def test_the_refusals_start_from_calls_that_pass(name):
+    _call(name, _moe_args())
+
+
+# each case changes one operand of a call that passes, and has to be refused for that operand
+@pytest.mark.parametrize("name,key,change,match", [
+    ("route", "score", lambda a: "tanh", "score must be one of"),
+    ("route", "logits", lambda a: a["logits"].double(), "logits has type torch.float64"),
+    ("route", "logits", lambda a: a["logits"][0], "logits must be 2-D"),
+    ("route", "logits", lambda a: a["logits"].t(), "unit column stride"),
+    ("route", "logits", lambda a: a["logits"][:1].expand(6, 16), "row stride of at least"),
+    ("route", "logits", lambda a: a["logits"].cpu(), "logits must be a CUDA tensor"),
+    ("route", "bias", lambda a: torch.zeros(15, device="cuda"), "bias has shape"),
+    ("route", "bias", lambda a: torch.zeros(16, device="cuda").bfloat16(), "bias has type"),
+    ("route", "bias", lambda a: torch.zeros(16), "bias is on cpu"),
+    ("route", "bias", lambda a: torch.zeros(32, device="cuda")[::2], "bias must be contiguous"),
+    ("route", "weights_out", lambda a: torch.zeros((6, 3), device="cuda"), "weights has shape"),
+    ("route", "ids_out", lambda a: torch.zeros((6, 2), device="cuda").long(), "ids has type"),
+    ("sort", "ids", lambda a: a["ids"].long(), "ids has type torch.int64"),
+    ("sort", "ids", lambda a: a["ids"][:, :1], "ids must be contiguous"),
+    ("sort", "ids", lambda a: a["ids"].cpu(), "ids must be a CUDA tensor"),
+    ("sort", "offsets_out", lambda a: torch.zeros(4, dtype=torch.int32, device="cuda"), "offsets has shape"),
+    ("sort", "order_out", lambda a: torch.zeros(11, dtype=torch.int32, device="cuda"), "order has shape"),
+    ("sort", "pos_out", lambda a: torch.zeros(12, dtype=torch.int32, device="cuda"), "pos has shape"),
+    ("experts", "x", lambda a: a["x"].float(), "x has type"),
+    ("experts", "x", lambda a: a["x"][0], "x must be 2-D"),
+    ("experts", "x", lambda a: torch.zeros((6, 128), device="cuda").bfloat16()[:, ::2], "unit column stride"),
+    ("experts", "x", lambda a: torch.zeros((6, 80), device="cuda").bfloat16(), "wq must be"),
+    ("experts", "wq", lambda a: a["wq"].view(torch.uint8), "wq has type"),
+    ("experts", "fmt", lambda a: qgd.FMT_FP8_DYNAMIC, "wq has type torch.int8"),
+    ("experts", "wq", lambda a: a["wq"][0], "wq must be"),
+    ("experts", "wq", lambda a: a["wq"].transpose(0, 1).contiguous().transpose(0, 1), "wq must be contiguous"),
+    ("experts", "wq", lambda a: a["wq"].cpu(), "wq is on cpu"),
+    ("experts", "sw", lambda a: a["sw"][:, :16].contiguous(), "sw has shape"),
+    ("experts", "sw", lambda a: a["sw"].double(), "sw has type"),
+    ("experts", "offsets", lambda a: a["offsets"][:4], "offsets has shape"),
+    ("experts", "offsets", lambda a: a["offsets"].long(), "offsets has type"),
+    ("experts", "order", lambda a: a["order"].long(), "order has type"),
+    ("experts", "order", lambda a: a["order"].tolist(), "order must be a tensor"),
+    ("experts", "act", lambda a: 2, "act must be"),
+    ("experts", "y", lambda a: torch.zeros((12, 64), device="cuda").bfloat16(), "y has shape"),
+    ("experts", "ws", lambda a: torch.zeros(1 << 20, dtype=torch.uint8), "ws must be"),
+    ("combine", "h", lambda a: a["h"].float(), "h has type"),
+    ("combine", "h", lambda a: a["h"][0], "h must be"),
+    ("combine", "pos", lambda a: a["pos"].long(), "pos has type"),
+    ("combine", "pos", lambda a: a["pos"].view(-1), "pos \\[tokens"),
+    ("combine", "weights", lambda a: a["weights"].bfloat16(), "weights has type"),
+    ("combine", "weights", lambda a: a["weights"][:, :1].contiguous(), "weights has shape"),
+    ("combine", "add", lambda a: a["h"][:5], "add has shape"),
+    ("combine", "add", lambda a: a["h"][:1].expand(6, 32), "row stride of at least"),
+    ("combine", "y", lambda a: torch.zeros((6, 32), device="cuda"), "y has type"),
+])
+def test_refusals_name_their_operand(name, key, change, match):
+    a = _moe_args()
+    a[key] = change(a)
+    with pytest.raises(ValueError, match=match):
+        _call(name, a)
