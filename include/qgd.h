@@ -397,9 +397,8 @@ QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int*
  *   rows     length of order and of y; rows of y at offsets[E] and behind are
  *            left as they were
  *   sw       fp32 [E][N] (or [E][2N])
- * Offsets ascend, as moe_sort's do; they are read on the device and clamped to
- * [0, min(rows, offsets[E])] (a row that lies in the ranges of several experts
- * all the same is one of theirs, not stated which); a source row outside
+ * Offsets are read on the device and clamped to [0, rows]; they ascend, as
+ * moe_sort's do (where they do not, no row of y is written); a source row outside
  * [0, x_rows) counts as zeros.  N % 16 == 0; K % 16 == 0, K <= 16384;
  * 1 <= E <= QGD_MAX_EXPERTS; (rows / 64 + E) * N / 64 * K / 256 and
  * (rows / 64 + 1) * E below 2^31, rows and the weight rows of all experts below

@@ -532,20 +532,19 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   griddep_launch_dependents();
   griddep_wait();  // offsets, codes and scales come from the kernels before
   // token tiles of the experts before e, as a running sum in blocks of experts
+  int descends = 0;
   {
-    // (no expert's rows go past offsets[E], also where the offsets do not ascend: the
-    // quantizer has coded none behind it)
-    const int live = offset_of(a, a.E);
     int carry = 0;
     if (threadIdx.x == 0) pre[0] = 0;
     for (int e0 = 0; e0 < a.E; e0 += kThreads) {
       const int e = e0 + threadIdx.x;
-      int v = 0;
+      int v = 0, below = 0;
       if (e < a.E) {
-        const int first = min(offset_of(a, e), live), cnt = min(offset_of(a, e + 1), live) - first;
+        const int first = offset_of(a, e), cnt = offset_of(a, e + 1) - first;
         off[e] = first;
         if (e == a.E - 1) off[a.E] = first + cnt;
         v = cnt > 0 ? (cnt + kTok - 1) / kTok : 0;
+        below = cnt < 0;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
         if (lane >= o) v += up;
       }
       if (lane == 31) ctl->scan[warp] = v;
-      __syncthreads();
+      descends |= __syncthreads_or(below);
       int before = carry, all = carry;
       for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) before += ctl->scan[i];
@@ -569,9 +568,10 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const int n_tiles = kPair ? (a.n_tiles + 1) / 2 : a.n_tiles;
-  // (no tiles where offsets that do not ascend list rows over and over: the host's
-  // check of the sizes, which keeps these numbers below 2^31, holds for ascending ones)
-  const int total = pre[a.E] <= a.P / kTok + a.E ? pre[a.E] * n_tiles : 0;
+  // (no tiles where the offsets do not ascend: ranges could hold rows over and over,
+  // more than the host's check of the sizes counts on, and rows behind offsets[E],
+  // which the quantizer has not coded)
+  const int total = descends ? 0 : pre[a.E] * n_tiles;
   const int U = total * nku;
   const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
   // Whole tiles leave workers idle at the end, split ones cost a hand-over (about

@@ -252,28 +252,30 @@ def test_route_as_many_rows_as_an_int_counts():
 
 
 @pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
-@pytest.mark.parametrize("scale", [1, 20, 150])
-def test_offsets_that_descend_end_at_the_last(fmt, scale):
-    # rows at offsets[E] and behind have no codes, whatever the offsets before say
+@pytest.mark.parametrize("E,scale", [(4, 1), (4, 20), (4, 150), (400, 1), (400, 150)])
+def test_offsets_that_descend_write_nothing(fmt, E, scale):
+    # rows could belong to several experts, and those at offsets[E] and behind have no codes
     int8 = fmt == "w8a8_int8"
-    E, K, N, rows = 4, 128, 48, 10 * scale
+    K, N, rows = 128, 48, 10 * scale
     wq, sw = _weights(E, N, K, int8, 1)
     x = torch.randn((rows, K), generator=_gen(1)).bfloat16()
     args = (qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC, x.cuda(), wq.cuda(), sw.cuda())
     need = qgd.qgd_experts_workspace_size(args[0], rows, 0, E, N, K)
-    for offsets in ([0, 3, 8, 9, 6], [0, 8, 8, 7, 6], [2, 9, 4, 4, -3], [7, 6, 9, 8, 0]):
-        off = scale * torch.tensor(offsets, dtype=torch.int32)
-        y = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
-        ws = torch.full((need,), 0x55, dtype=torch.uint8, device="cuda")  # what uncoded rows would hold
-        qgd.qlinear_experts_bf16(*args, off.cuda(), y=y, ws=ws)
-        cut = off.clamp(min=0, max=max(int(off[-1]), 0))
-        n = int(cut[-1])
-        assert (y[n:] == 7.0).all()
-        ref, mag = moelib.experts(x, wq, sw, cut, None, 1, False, int8)
-        tol = moelib.experts_tolerance(ref, mag, K, False, int8)
-        first = int(cut[0])
-        assert (y[:first] == 7.0).all()
-        moelib.close(y[first:n], ref[first:n], tol[first:n])
+    for place in {0, E - 4}:  # descents among the first and the last experts
+        for offsets in ([0, 3, 8, 9, 6], [0, 8, 8, 7, 6], [2, 9, 4, 4, -3], [7, 6, 9, 8, 0], [0, 3, 5, 8, 9]):
+            off = torch.full((E + 1,), offsets[-1] if place == 0 else offsets[0], dtype=torch.int32)
+            off[place:place + 5] = torch.tensor(offsets, dtype=torch.int32)
+            off *= scale
+            y = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            ws = torch.full((need,), 0x55, dtype=torch.uint8, device="cuda")  # what uncoded rows would hold
+            qgd.qlinear_experts_bf16(*args, off.cuda(), y=y, ws=ws)
+            if offsets == sorted(offsets):
+                ref, mag = moelib.experts(x, wq, sw, off, None, 1, False, int8)
+                n = int(off[-1])
+                moelib.close(y[:n], ref[:n], moelib.experts_tolerance(ref, mag, K, False, int8)[:n])
+                assert (y[n:] == 7.0).all()
+            else:
+                assert (y == 7.0).all()
 
 
 # ---------------------------------------------------------------------------
