@@ -403,3 +403,79 @@ def test_refusals_name_their_operand(name, key, change, match):
     a[key] = change(a)
     with pytest.raises(ValueError, match=match):
         _call(name, a)
+
+
+# ---------------------------------------------------------------------------
+# behind copies, wide layers
+# ---------------------------------------------------------------------------
+def test_calls_wait_for_the_copies_before_them():
+    # copies of a few microseconds in front of the calls, on a stream and inside a graph
+    T, E, k, K, N = 16384, 256, 8, 512, 64
+    wq, sw = (t.cuda() for t in _weights(E, N, K, True, 1))
+    lg, x = torch.empty((T, E), device="cuda"), torch.empty((T, K), device="cuda").bfloat16()
+    ids, w, pos = (torch.empty((T, k), dtype=d, device="cuda") for d in (torch.int32, torch.float32, torch.int32))
+    h = torch.empty((T * k, N), device="cuda").bfloat16()
+
+    def calls(src):
+        lg.copy_(src["lg"])
+        rw, ri = qgd.moe_route(lg, k)
+        ids.copy_(src["ids"])
+        off, order, p = qgd.moe_sort(ids, E)
+        x.copy_(src["x"])
+        y = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, x, wq, sw, off, order=order, top_k=k)
+        w.copy_(src["w"])
+        pos.copy_(p)
+        h.copy_(y)
+        return [rw, ri, off, order, p, y, qgd.moe_combine(h, pos, w)]
+
+    def source(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        return dict(lg=torch.randn((T, E), generator=g, device="cuda"),
+                    ids=torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32),
+                    x=torch.randn((T, K), generator=g, device="cuda").bfloat16(),
+                    w=torch.rand((T, k), generator=g, device="cuda"))
+
+    def settled(src):  # every copy and call on its own
+        out = []
+        for fn in (lambda: qgd.moe_route(src["lg"], k), lambda: qgd.moe_sort(src["ids"], E)):
+            out += fn()
+            torch.cuda.synchronize()
+        out.append(qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8, src["x"], wq, sw, out[2], order=out[3], top_k=k))
+        torch.cuda.synchronize()
+        return out + [qgd.moe_combine(out[5], out[4], src["w"])]
+
+    src = source(0)
+    calls(src)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = calls(src)
+    for seed in range(1, 4):
+        new = source(seed)
+        want = settled(new)
+        for got in (calls(new), None):
+            if got is None:
+                for n, t in src.items():
+                    t.copy_(new[n])
+                graph.replay()
+                got = held
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", ["w8a8_int8", "fp8_dynamic"])
+@pytest.mark.parametrize("T,k,E,K,N,act", [(1, 8, 256, 7168, 64, True), (33, 8, 256, 7168, 32, False),
+                                           (90, 6, 1024, 256, 32, True), (2600, 8, 1024, 64, 16, False),
+                                           (300, 8, 8, 7168, 48, True), (700, 2, 4, 16384, 32, False)])
+def test_experts_wide_and_many(fmt, T, k, E, K, N, act):
+    int8 = fmt == "w8a8_int8"
+    g = _gen(T + E)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    off, order, _ = (torch.from_numpy(v) for v in moelib.sort(ids, E))
+    x = torch.randn((T, K), generator=g).bfloat16()
+    wq, sw = _weights(E, N * (2 if act else 1), K, int8, 5)
+    y = qgd.qlinear_experts_bf16(qgd.FMT_W8A8_INT8 if int8 else qgd.FMT_FP8_DYNAMIC, x.cuda(), wq.cuda(), sw.cuda(),
+                                 off.cuda(), order=order.cuda(), top_k=k,
+                                 act=qgd.ACT_SILU_MUL if act else qgd.ACT_NONE)
+    ref, mag = moelib.experts(x, wq, sw, off, order, k, act, int8)
+    moelib.close(y, ref, moelib.experts_tolerance(ref, mag, K, act, int8))
