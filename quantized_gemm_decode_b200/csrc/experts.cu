@@ -29,7 +29,6 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <utility>
 
 #include "qgd_internal.h"
 #include "quantcore.cuh"
@@ -828,23 +827,6 @@ __global__ void __launch_bounds__(Layout<kTok, kKps, kPair, kGroups, kAct>::kThr
     if constexpr (kPair) tmem_dealloc_pair(tmem, kCols);
     else tmem_dealloc(tmem, kCols);
   }
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 constexpr int kManyRows = 1184;  // a wave of 8 CTAs on each of 148 SMs
