@@ -367,7 +367,7 @@ typedef struct {
  * that makes the choice value -inf or NaN) keeps its expert from being
  * chosen; +inf counts as the largest fp32.  Slots left without an expert get
  * id -1 and weight 0.  1 <= E <= QGD_MAX_EXPERTS; ldl >= E; logits aligned to
- * their type. */
+ * their type.  The outputs must not overlap the inputs or one another. */
 QGD_API qgd_status moe_route(const void* logits, int logits_dtype, int T, int E, int ldl, const float* bias,
                              const qgd_route* route, float* weights, int* ids, void* stream);
 
@@ -376,8 +376,8 @@ QGD_API qgd_status moe_route(const void* logits, int logits_dtype, int T, int E,
  * positions offsets[e] .. offsets[e+1] - 1; order [pairs]: the pair at each
  * sorted position, -1 behind the last; pos [pairs]: the sorted position of
  * each pair, -1 where it was dropped.  pairs == 0 writes offsets only (all
- * zero).  Workspace: qgd_moe_sort_workspace_size() bytes, 16-byte aligned
- * (NULL when 0). */
+ * zero).  The outputs must not overlap ids or one another.  Workspace:
+ * qgd_moe_sort_workspace_size() bytes, 16-byte aligned (NULL when 0). */
 QGD_API size_t qgd_moe_sort_workspace_size(int pairs, int E);
 QGD_API qgd_status moe_sort(const int* ids, int pairs, int E, int* offsets, int* order, int* pos, void* ws,
                             size_t ws_bytes, void* stream);
@@ -416,7 +416,7 @@ QGD_API qgd_status qlinear_experts_bf16(int fmt, const void* x_bf16, int ldx, in
  * h bf16 [rows][H]; pos int32 and weights fp32 [T][top_k]; add bf16 [T]
  * rows lda elements apart, or NULL for zero; y bf16 [T][H].  H % 8 == 0;
  * top_k <= QGD_MAX_TOP_K; h, add and y 16-byte aligned, lda % 8 == 0.  y may
- * be add, and must not overlap h. */
+ * be add where lda == H; else it must not overlap the inputs. */
 QGD_API qgd_status moe_combine(const void* h_bf16, int rows, const int* pos, const float* weights,
                                const void* add_bf16, int lda, void* y_bf16, int T, int top_k, int H, void* stream);
 

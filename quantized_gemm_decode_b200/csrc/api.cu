@@ -747,6 +747,9 @@ struct ExpertPlan {
 // x_rows: rows of x behind an order, or 0 without one
 ExpertPlan expert_plan(int rows, int x_rows, int E, int N, int K, bool act) {
   ExpertPlan p;
+  // (by the average alone: how the rows fall is known on the device only.  Pairs that
+  // were dropped count as rows, and a hot expert among idle ones reads its weights
+  // once per tile, so a call with many of either would do better with another tile.)
   // few rows per expert: 64- or 128-token tiles whose K range is shared out
   // over all SMs (streaming the weights once bounds them); many: 256-token
   // tiles of CTA pairs

@@ -18,11 +18,13 @@
 // Few rows per expert: 64- or 128-token tiles, bound by the one pass over the
 // weights; (tile, K unit) units are dealt out over all SMs where whole tiles would
 // leave too many idle.  Measured on B200, 32 tokens x 8 of 64 experts, 4096 x 1024
-// e4m3 weights: 44.2 us per call, of which the weights stream for 40.5 us (6.5
+// e4m3 weights: 44 us per call (replayed from a graph), of which the weights stream for 40.5 us (6.5
 // TB/s) after 5.5 us of quantizer, hand-over and tile search.  Many: 256-token
 // tiles of CTA pairs, bound by the MMA, whose operands and the copies that refill
 // them share an SM's shared-memory bandwidth: 8192 tokens x 8 of 64 experts, 2048 x
-// 4096 int8 gate / up weights: 2.8 PFLOP/s in the GEMM, 484 us per call.
+// 4096 int8 gate / up weights: 2.8 PFLOP/s in the GEMM; 472 to 494 us per call in
+// short runs (replayed from a graph, box by box), 554 to 569 where calls one behind
+// the other bring the GPU to its power limit.
 //
 // Warp roles: warp 0 issues TMA loads, warp 1 owns TMEM and issues MMAs, the
 // groups of four warps behind them drain the accumulator.  Every wait is bounded.

@@ -26,7 +26,10 @@ constexpr uint32_t kFull = 0xffffffffu;
 // one (and for sums of two scores) a row is first chosen from 32-bit values of
 // known error; only where two values that decide something lie closer than
 // that error, and are not the same logit with the same bias, the row is chosen
-// again in 64 bits (a few rows in a hundred of random ones).  Weights are computed from the chosen logits in 64 bits.
+// again in 64 bits (of random rows of 256 experts with a bias, 0.15 % with sigmoid
+// scores and 0.4 to 0.7 % with softmax).  Weights are computed from the chosen
+// logits in 64 bits; the 64-bit sum that divides them is of the chosen ones' scores,
+// or, for a softmax that is not renormalised, of all exponentials, each within 2^-22.
 // Bound by its instructions (about 1100 a row of 256 experts in 8 groups, 8
 // chosen): 28 us for 16384 such rows, 3.1 us for one; 64-bit values throughout
 // took 91 and 9.3 us.
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kVPT <= 8 ? 8 : 1) route_ker
 // second pass over the same pairs places them, 32 at a time: a pair's rank among
 // the 32 is the number of lower lanes with the same expert.  One block does a
 // decode step; more blocks first count their pairs in a kernel of their own.
-// Bound by latency: 1.9 us for 256 pairs, 12.7 us for 262144 over 256 experts.
+// Bound by latency: 1.8 us for 256 pairs, 12.4 us for 262144 over 256 experts.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
