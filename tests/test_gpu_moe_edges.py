@@ -304,6 +304,22 @@ def test_sort_of_many_pairs(P, E):
     _check_sort(ids, E)
 
 
+def test_sort_as_many_pairs_as_an_int_counts():
+    # all but the last pairs go to expert 1; 34 GB
+    P, tail = (1 << 31) - 1, [2, -1, 0, 1, 2, 7]
+    ids = torch.ones(P, dtype=torch.int32, device="cuda")
+    ids[-6:] = torch.tensor(tail, dtype=torch.int32)
+    off, order, pos = qgd.moe_sort(ids, 3)
+    assert off.tolist() == [0, 1, P - 4, P - 2]
+    assert order[0] == P - 4 and order[P - 5] == P - 3 and order[P - 4:].tolist() == [P - 6, P - 2, -1, -1]
+    assert pos[-6:].tolist() == [P - 4, -1, 0, P - 5, P - 3, -1]
+    for a in range(0, P - 6, 1 << 29):  # the others keep their order, one place up
+        b = min(a + (1 << 29), P - 6)
+        run = torch.arange(a, b, dtype=torch.int32, device="cuda")
+        assert torch.equal(order[a + 1:b + 1], run)
+        assert torch.equal(pos[a:b], run + 1)
+
+
 def test_sort_time_grows_with_the_pairs():
     # (with every block adding up all blocks' counts, 64 M pairs took 780 ms, and 2 G would take minutes)
     def ms(P):
